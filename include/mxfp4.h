@@ -322,6 +322,167 @@ MXFP4_API mxfp4_status mxfp4_inverse_transpose(const float* m, int32_t n, float*
  *   past the first such factor). */
 MXFP4_API mxfp4_status mxfp4_smooth_weight_factors(const float* r, int64_t k, float* out);
 
+/* ---------------------------------------------------------------------------
+ * Feed-forward operators: what a transformer block needs around its MXFP4
+ * GEMMs.  A norm that takes the residual add before it and quantizes its
+ * result (mxfp4_norm, mxfp4_norm_quantize), a GEMM whose epilogue adds the
+ * bias, applies the activation, the gate and the residual, or requantizes
+ * (mxfp4_gemm_epilogue, mxfp4_gemm_epilogue_requant), and the gated form with
+ * both projections and their product in one kernel (mxfp4_gemm_glu,
+ * mxfp4_gemm_glu_requant).  A feed-forward block is then three launches with
+ * MXFP4 activations in between.  All arithmetic between the operands and the
+ * stored result is fp32, rounded once to the output type.  Dense outputs carry
+ * NaN and infinities as the formulas do; MXFP4 outputs are defined for finite
+ * values.  The library is inference only: no gradients. */
+
+/* Activations.  GELU uses the Abramowitz and Stegun 7.1.26 rational
+ * approximation of erf (absolute error below 1.5e-7); GELU_TANH is
+ * x * sigmoid(2 sqrt(2/pi) (x + 0.044715 x^3)), the tanh form. */
+typedef enum {
+    MXFP4_ACT_NONE = 0,
+    MXFP4_ACT_RELU = 1,
+    MXFP4_ACT_SILU = 2,
+    MXFP4_ACT_GELU = 3,
+    MXFP4_ACT_GELU_TANH = 4
+} mxfp4_act;
+
+/* Statistics of a norm: RMS  z = r / sqrt(mean(r^2) + eps);
+ * LAYER  z = (r - mean(r)) / sqrt(mean((r - mean(r))^2) + eps). */
+typedef enum {
+    MXFP4_NORM_RMS = 0,
+    MXFP4_NORM_LAYER = 1
+} mxfp4_norm_kind;
+
+/* A norm over rows of d elements, with what surrounds it in a block:
+ *   p = post_norm ? norm(x) * post_weight : x
+ *   r = residual_scale * residual + gate[g] * p     (g = row / group_rows)
+ *   y = (norm(r) * weight + bias) * (1 + scale[g]) + shift[g]
+ * with the absent (NULL) tensors left out; without residual, r = gate[g] * p.
+ * Both norms are of `kind` with `eps`.  r is written to residual_out, rounded
+ * to r_dtype; the second norm reads r before that rounding.
+ *   x             device [rows][ld_x] of x_dtype
+ *   residual      device [rows][ld_r] of r_dtype, or NULL
+ *   residual_out  device [rows][ld_ro] of r_dtype, or NULL; may be `residual`
+ *                 itself with the same stride (or x, where the types agree)
+ *   post_weight, weight, bias   device [d] of vec_dtype, or NULL
+ *   gate, scale, shift          device [ceil(rows / group_rows)][ld_vec] of
+ *                 vec_dtype, or NULL; group_rows >= 1 if any is given
+ * mxfp4_norm takes pointers aligned to their elements (16-byte aligned
+ * pointers and row strides, with d a multiple of 8, take the vector path);
+ * mxfp4_norm_quantize needs 16-byte aligned pointers and row strides. */
+typedef struct {
+    int32_t kind, x_dtype, r_dtype, vec_dtype;
+    int64_t rows, d;
+    const void* x;
+    int64_t ld_x;
+    const void* residual;
+    int64_t ld_r;
+    void* residual_out;
+    int64_t ld_ro;
+    const void* post_weight;
+    const void* weight;
+    const void* bias;
+    const void* gate;
+    const void* scale;
+    const void* shift;
+    int64_t ld_vec, group_rows;
+    float residual_scale, eps;
+    int32_t post_norm;
+    int32_t reserved;      /* must be 0 */
+} mxfp4_norm_args;
+
+/* The norm with a dense result: y device [rows][ld_y] of y_dtype, or NULL for
+ * residual_out alone.
+ * Errors: INVALID_ARG for null a or x (when rows > 0), bad kinds or dtypes,
+ *   negative rows, d < 1, strides below d, post_weight without post_norm,
+ *   group_rows < 1 with a grouped tensor, eps < 0 or not finite, neither y nor
+ *   residual_out, reserved != 0; UNSUPPORTED for d > 65536, rows >= 2^30 or
+ *   pointers not aligned to their elements; HIP if the launch fails. */
+MXFP4_API mxfp4_status mxfp4_norm(const mxfp4_norm_args* a, void* y, int32_t y_dtype, int64_t ld_y,
+                                  void* stream);
+
+/* The norm with an MXFP4 result: codes and scales equal mxfp4_quantize_rotate
+ * with `rot` applied to mxfp4_norm's fp32 y, bit for bit.
+ *   rot     NULL / NONE, HADAMARD32, SMOOTH or KRON.
+ *   layout, codes, scales  as for mxfp4_quantize_rotate (TILED: the padding
+ *           rows are not written).
+ * Errors: as mxfp4_norm (y aside), INVALID_ARG for null codes or scales,
+ *   d % 32 != 0 (d % 128 for TILED), a bad layout or rotation; UNSUPPORTED for
+ *   pointers or row strides that are not 16-byte aligned (TILED scales: 4),
+ *   rows * d / 32 >= 2^31, or KRON with d > 16384; HIP if the launch fails. */
+MXFP4_API mxfp4_status mxfp4_norm_quantize(const mxfp4_norm_args* a, const mxfp4_rotation* rot, int32_t layout,
+                                           uint8_t* codes, uint8_t* scales, void* stream);
+
+/* Epilogue of a GEMM: Y = residual + gate[g] * act(A * B^T + bias), with the
+ * absent (NULL) tensors left out and g = row / group_rows.
+ *   bias      device [n] of vec_dtype, or NULL
+ *   gate      device [ceil(m / group_rows)][ld_gate] of vec_dtype, or NULL
+ *   residual  device [m][ld_res] of res_dtype, or NULL; may be Y itself with
+ *             Y's type and stride (no other overlap) */
+typedef struct {
+    int32_t act;           /* mxfp4_act */
+    int32_t vec_dtype;     /* mxfp4_dtype of bias and gate */
+    const void* bias;
+    const void* gate;
+    int64_t ld_gate, group_rows;
+    const void* residual;
+    int64_t ld_res;
+    int32_t res_dtype;
+    int32_t reserved;      /* must be 0 */
+} mxfp4_epilogue;
+
+/* mxfp4_gemm with an epilogue (NULL: none).  Operands, sizes and Y as for
+ * mxfp4_gemm; bias, gate and residual need the alignment of their elements.
+ * Errors: as mxfp4_gemm; INVALID_ARG for a bad activation or dtype, ld_gate or
+ *   ld_res below n, group_rows < 1 with a gate, reserved != 0; UNSUPPORTED for
+ *   pointers not aligned to their elements, or sizes past the grid
+ *   (ROWMAJOR, m > 64 and k % 128 != 0: m < 2^22). */
+MXFP4_API mxfp4_status mxfp4_gemm_epilogue(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m,
+                                           const uint8_t* b_codes, const uint8_t* b_scales, int64_t n,
+                                           int64_t k, int32_t layout, const mxfp4_epilogue* e, void* y,
+                                           int32_t y_dtype, int64_t ld_y, void* stream);
+
+/* The same with an MXFP4 output along N, optionally rotated first: Y equals
+ * mxfp4_quantize_rotate with `rot` applied to mxfp4_gemm_epilogue's fp32 Y,
+ * bit for bit.  `e` may hold the activation and the bias only; rot is NULL /
+ * NONE or HADAMARD32.
+ * Errors: as mxfp4_gemm_epilogue; INVALID_ARG for null outputs, a bad y_layout
+ *   or a bad rotation; UNSUPPORTED for a gate or a residual, another
+ *   rotation, n % 32 != 0 (n % 128 for a TILED output), or outputs not
+ *   aligned (codes 16, scales 4 bytes). */
+MXFP4_API mxfp4_status mxfp4_gemm_epilogue_requant(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m,
+                                                   const uint8_t* b_codes, const uint8_t* b_scales, int64_t n,
+                                                   int64_t k, int32_t layout, const mxfp4_epilogue* e,
+                                                   const mxfp4_rotation* rot, uint8_t* y_codes,
+                                                   uint8_t* y_scales, int32_t y_layout, void* stream);
+
+/* Gated projections H = act(A * G^T + bias_g) * (A * U^T + bias_u) in one
+ * kernel: G (the gate projection) and U (the up projection) are two weights of
+ * n rows each, in `layout`, as mxfp4_quantize_rotate leaves them. */
+typedef struct {
+    int32_t act;           /* mxfp4_act */
+    int32_t vec_dtype;     /* mxfp4_dtype of the biases */
+    const uint8_t* g_codes;
+    const uint8_t* g_scales;
+    const uint8_t* u_codes;
+    const uint8_t* u_scales;
+    const void* bias_g;    /* device [n], or NULL */
+    const void* bias_u;    /* device [n], or NULL */
+    int32_t reserved;      /* must be 0 */
+} mxfp4_glu;
+
+/* Errors: as mxfp4_gemm (each weight checked as B), INVALID_ARG for a null w,
+ *   a bad activation or dtype, reserved != 0. */
+MXFP4_API mxfp4_status mxfp4_gemm_glu(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m,
+                                      const mxfp4_glu* w, int64_t n, int64_t k, int32_t layout, void* y,
+                                      int32_t y_dtype, int64_t ld_y, void* stream);
+
+/* The same with an MXFP4 output, as mxfp4_gemm_epilogue_requant. */
+MXFP4_API mxfp4_status mxfp4_gemm_glu_requant(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m,
+                                              const mxfp4_glu* w, int64_t n, int64_t k, int32_t layout,
+                                              const mxfp4_rotation* rot, uint8_t* y_codes, uint8_t* y_scales,
+                                              int32_t y_layout, void* stream);
+
 /* Static description of a status code (never NULL). */
 MXFP4_API const char* mxfp4_status_string(int32_t status);
 

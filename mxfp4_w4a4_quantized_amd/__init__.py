@@ -12,6 +12,8 @@ C-ABI calls declared in include/mxfp4.h:
   quantize_weight(w, rot)            offline weight quantization with the
                                      weight side of the rotation
   inverse_transpose(m)               host helper for the Kronecker weight fold
+  norm, norm_quantize, gemm_epilogue, gemm_epilogue_requant, gemm_glu,
+  gemm_glu_requant, ffn              the feed-forward operators (feedforward.py)
 
 Layouts: ROWMAJOR (codes [rows, k/2], scales [rows, k/32]) or TILED, the
 GEMM-native layout of include/mxfp4.h (256-row tiles x 128-element stages,
@@ -49,7 +51,8 @@ EXPORTED = ("mxfp4_quantize_rotate", "mxfp4_quantize_fit", "mxfp4_gemm", "mxfp4_
             "mxfp4_linear_small", "mxfp4_linear_small_noalloc", "mxfp4_linear_small_workspace",
             "mxfp4_tiled_bytes",
             "mxfp4_inverse_transpose", "mxfp4_smooth_weight_factors", "mxfp4_status_string",
-            "mxfp4_abi_version")
+            "mxfp4_abi_version", "mxfp4_norm", "mxfp4_norm_quantize", "mxfp4_gemm_epilogue",
+            "mxfp4_gemm_epilogue_requant", "mxfp4_gemm_glu", "mxfp4_gemm_glu_requant")
 LINEAR_SMALL_MAX_M = 64
 
 
@@ -103,6 +106,8 @@ def lib() -> ctypes.CDLL:
     L.mxfp4_status_string.argtypes = [i32]
     L.mxfp4_abi_version.restype = i32
     L.mxfp4_abi_version.argtypes = []
+    from .feedforward import declare
+    declare(L)
     _lib = L
     return L
 
@@ -488,3 +493,7 @@ def inverse_transpose(m: np.ndarray) -> np.ndarray:
     st = lib().mxfp4_inverse_transpose(m.ctypes.data, n, out.ctypes.data)
     _check(st, "mxfp4_inverse_transpose")
     return out
+
+
+from .feedforward import (Epilogue, Norm, ffn, gemm_epilogue, gemm_epilogue_requant,  # noqa: E402,F401
+                          gemm_glu, gemm_glu_requant, norm, norm_quantize)

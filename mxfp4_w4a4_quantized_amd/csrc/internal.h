@@ -95,4 +95,58 @@ int64_t linear_small_workspace_bytes(int64_t m, int64_t k);
 constexpr int64_t kLinearStaticScratchBytes = int64_t(4) << 20;
 hipError_t linear_small_static_scratch(void** ptr, hipStream_t s);
 
+// GEMM with a feed-forward epilogue (gemm_fused_small.hip,
+// gemm_fused_large.hip): Y = residual + gate[g] * act(A B^T + bias), or, with
+// glu, H = act(A B^T + bias) * (A U^T + bias_u); dense (g.y) or MXFP4 (g.q_*,
+// after an optional Hadamard-32 along N; no gate or residual then).
+struct FusedArgs {
+  GemmArgs g;
+  bool glu = false;
+  const uint8_t* u_codes = nullptr;   // second weight, n rows, same layout
+  const uint8_t* u_scales = nullptr;
+  int32_t act = 0;                    // mxfp4_act
+  bool vec_bf16 = false;              // type of the vectors below
+  const void* bias = nullptr;         // n
+  const void* bias_u = nullptr;       // n
+  const void* gate = nullptr;         // [groups][ld_gate]
+  int64_t ld_gate = 0;
+  uint32_t group_rows = 1;            // rows of Y per gate row
+  const void* residual = nullptr;     // [m][ld_res]
+  int64_t ld_res = 0;
+  bool res_bf16 = false;
+  bool h32 = false;
+};
+
+hipError_t launch_fused_small(const FusedArgs& a, hipStream_t s);
+
+// Norm with residual, gate and modulation (norm.hip); dense or MXFP4 result.
+struct NormArgs {
+  const void* x;
+  const void* residual;
+  void* residual_out;
+  const void *post_weight, *weight, *bias;    // d
+  const void *gate, *scale, *shift;           // [groups][ld_vec]
+  int64_t ld_x, ld_r, ld_ro, ld_vec;
+  uint32_t rows, d, group_rows;
+  bool x_bf16, r_bf16, vec_bf16;
+  bool layer, post_norm;
+  bool vec;                                   // every pointer and stride 16-byte aligned, d % 8 == 0
+  float residual_scale, eps;
+  // dense result (may be null)
+  void* y = nullptr;
+  int64_t ld_y = 0;
+  bool y_bf16 = false;
+  // MXFP4 result (may be null)
+  uint8_t* codes = nullptr;
+  uint8_t* scales = nullptr;
+  bool tiled = false;
+  int32_t rot = 0, p = 0, q = 0;              // mxfp4_rot_kind and its factors
+  const float* fa = nullptr;
+  const float* fb = nullptr;
+};
+
+constexpr int64_t kNormMaxD = 65536;          // row length
+constexpr int64_t kNormMaxDKron = 16384;      // and with KRON, whose rows pass through LDS
+hipError_t launch_norm(const NormArgs& a, hipStream_t s);
+
 }  // namespace mxfp4

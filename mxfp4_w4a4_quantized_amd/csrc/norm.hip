@@ -1,0 +1,438 @@
+// Norm with what surrounds it in a transformer block, for gfx950:
+//   p = [norm(x) * post_weight | x]
+//   r = residual_scale * residual + gate[g] * p        -> residual_out
+//   y = (norm(r) * weight + bias) * (1 + scale[g]) + shift[g]
+// y dense, or quantized to MXFP4 after an optional block transform.
+//
+// Bound by HBM: x and the residual are read once, r and y (or 4.25 bits an
+// element of y) written once.  WPR waves own a row; every lane keeps its
+// columns of the row in registers as chunks of 8 consecutive elements (16
+// bytes of bf16: a wave's load instruction covers 1 KiB of the row), so the
+// statistics, which need the whole row, cost no second read.  Statistics are
+// fp32: per-lane sums, then a butterfly over the wave, then (WPR > 1) one LDS
+// exchange; the layer norm's variance is the mean square of the centred
+// values, not a difference of moments.
+//
+// MXFP4 result: a 32-element block is four neighbouring lanes (a quad), so the
+// block amax and the Hadamard's strides 8 and 16 are quad permutes and a lane
+// stores the 4 code bytes of its chunk.  A Kronecker transform mixes all 32
+// elements: there the row passes through LDS and Q lanes take a block.
+// Every operation from y on is the quantizer's, in its order, so codes and
+// scales equal quantizing the fp32 y bit for bit.
+#include "internal.h"
+#include "block_quant.h"
+
+namespace mxfp4 {
+namespace {
+
+using namespace blockq;
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, b2));
+}
+
+// Eight consecutive elements at column c of a row (columns past d read as 0;
+// VEC: whole aligned chunks).
+template <bool VEC>
+__device__ __forceinline__ void load8(const void* base, bool bf16, int64_t off, uint32_t c, uint32_t d, float (&v)[8]) {
+  if constexpr (VEC) {
+    if (bf16) {
+      const u32x4 q = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + off + c);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = bf16_lo(q[j]);
+        v[2 * j + 1] = bf16_hi(q[j]);
+      }
+    } else {
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + off + c);
+      const float4 a = p[0], b = p[1];
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = 0.0f;
+      if (c + j < d)
+        v[j] = bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(base)[off + c + j] << 16)
+                    : static_cast<const float*>(base)[off + c + j];
+    }
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(void* base, bool bf16, int64_t off, uint32_t c, uint32_t d, const float (&v)[8]) {
+  if constexpr (VEC) {
+    if (bf16) {
+      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(base) + off + c) =
+          u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+    } else {
+      float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + off + c);
+      p[0] = make_float4(v[0], v[1], v[2], v[3]);
+      p[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (c + j >= d) continue;
+      if (bf16) static_cast<uint16_t*>(base)[off + c + j] = (uint16_t)pack_bf16(v[j], 0.0f);
+      else static_cast<float*>(base)[off + c + j] = v[j];
+    }
+  }
+}
+
+// Lane i's value from lane i ^ 1 or i ^ 2 of its quad.
+template <int X>
+__device__ __forceinline__ float quad_xor(float v) {
+  constexpr int ctrl = X == 1 ? 0xB1 : 0x4E;   // quad_perm [1,0,3,2] / [2,3,0,1]
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), ctrl, 0xF, 0xF, true));
+}
+
+template <int WPR>
+__device__ __forceinline__ float row_sum(float v, float* slot, int wave) {
+  v += quad_xor<1>(v);
+  v += quad_xor<2>(v);
+#pragma unroll
+  for (int o = 4; o < 64; o <<= 1) v += __shfl_xor(v, o);
+  if constexpr (WPR > 1) {
+    if ((threadIdx.x & 63) == 0) slot[wave] = v;
+    __syncthreads();
+    v = slot[0];
+#pragma unroll
+    for (int i = 1; i < WPR; ++i) v += slot[i];
+  }
+  return v;
+}
+
+// The scale of norm(v) over the row's d elements; centres v for a layer norm
+// (columns past d stay 0).
+template <int EPL, int WPR>
+__device__ __forceinline__ float statistics(const NormArgs& a, float (&v)[EPL][8], uint32_t c0, float* slots, int wave) {
+  const float inv_d = 1.0f / (float)a.d;
+  if (a.layer) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += v[i][j];
+    const float mean = row_sum<WPR>(s, slots, wave) * inv_d;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = c0 + i * 512 * WPR + j < a.d ? v[i][j] - mean : 0.0f;
+  }
+  float q = 0.0f;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q = __builtin_fmaf(v[i][j], v[i][j], q);
+  return __builtin_amdgcn_rsqf(__builtin_fmaf(row_sum<WPR>(q, slots + WPR, wave), inv_d, a.eps));
+}
+
+__device__ __forceinline__ int tiled_swz(int r) { return ((r >> 1) ^ (r >> 2)) & 3; }
+
+// Where block `blk` of a row goes.
+struct BlockOut {
+  uint8_t* code;    // 16 bytes
+  uint8_t* scale;
+};
+
+__device__ __forceinline__ BlockOut block_out(const NormArgs& a, uint32_t row, uint32_t blk) {
+  if (a.tiled) {
+    const uint32_t r = row % kTileRows, cb = blk & 3u;
+    const uint64_t ts = (uint64_t)(row / kTileRows) * (a.d >> 7) + (blk >> 2);
+    return {a.codes + ts * (kTileRows * 64) + r * 64 + 16 * (cb ^ tiled_swz((int)r)),
+            a.scales + ts * (kTileRows * 4) + r * 4 + cb};
+  }
+  const uint64_t b = (uint64_t)row * (a.d >> 5) + blk;
+  return {a.codes + 16 * b, a.scales + b};
+}
+
+// Quantizes one chunk per lane; the four lanes of a quad hold one block.
+template <int ROT>
+__device__ __forceinline__ void quantize_quad(const NormArgs& a, float (&v)[8], uint32_t row, uint32_t c, int lane) {
+  if constexpr (ROT == 3) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = v[j] * a.fa[c + j];
+  }
+  if constexpr (ROT == 1) {
+#pragma unroll
+    for (int h = 1; h < 8; h <<= 1)
+#pragma unroll
+      for (int i = 0; i < 8; i += 2 * h)
+#pragma unroll
+        for (int j = i; j < i + h; ++j) {
+          const float u = v[j], w = v[j + h];
+          v[j] = u + w;
+          v[j + h] = u - w;
+        }
+    // strides 8 and 16 across the quad: the lower lane forms u + w, the upper
+    // one u - w from its partner's u
+    const uint32_t s1 = (lane & 1) ? 0x80000000u : 0u, s2 = (lane & 2) ? 0x80000000u : 0u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = quad_xor<1>(v[j]) + __uint_as_float(__float_as_uint(v[j]) ^ s1);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = quad_xor<2>(v[j]) + __uint_as_float(__float_as_uint(v[j]) ^ s2);
+    const float k = __uint_as_float(0x3E3504F3u);   // nearest fp32 to 1/sqrt(32)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = v[j] * k;
+  }
+  float am = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) am = fmaxf(am, fabsf(v[j]));
+  am = fmaxf(am, quad_xor<1>(am));
+  am = fmaxf(am, quad_xor<2>(am));
+  const uint32_t sbyte = sbyte_of_amax(am);
+  const float scale = scale_of(sbyte);
+  uint32_t w = 0;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], scale, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], scale, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], scale, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], scale, 3);
+  if (c >= a.d) return;
+  const BlockOut o = block_out(a, row, c >> 5);
+  reinterpret_cast<uint32_t*>(o.code)[lane & 3] = w;
+  if ((lane & 3) == 0) *o.scale = (uint8_t)sbyte;
+}
+
+// One Kronecker-transformed block over Q lanes: lane k forms column k of both
+// stages, U[j][k] for every j and then y[Q i + k] -- the chains of the one-lane
+// transform in their order -- and the group merges the block amax and the code
+// nibbles with butterflies (an exact max and an OR).
+template <int P, int Q>
+__device__ __forceinline__ void kron_block(const NormArgs& a, const float* blk, uint32_t row, uint32_t b, int k) {
+  float u[P];
+#pragma unroll
+  for (int j = 0; j < P; ++j) u[j] = a.fb[k * Q] * blk[Q * j];
+#pragma unroll
+  for (int l = 1; l < Q; ++l) {
+    const float f = a.fb[k * Q + l];
+#pragma unroll
+    for (int j = 0; j < P; ++j) u[j] = __builtin_fmaf(f, blk[Q * j + l], u[j]);
+  }
+  auto out = [&](int i) {   // y[Q i + k]
+    float acc = a.fa[i * P] * u[0];
+#pragma unroll
+    for (int j = 1; j < P; ++j) acc = __builtin_fmaf(a.fa[i * P + j], u[j], acc);
+    return acc;
+  };
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+  float am = 0.0f, scale;
+  uint32_t sbyte;
+  auto put = [&](int i, float v) {   // its code, into nibble Q i + k of the block
+    const int e = Q * i + k;
+    const uint32_t c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v, 0.0f, scale, 0) & 0xFu;
+    const uint32_t sh = 4u * (uint32_t)(e & 7);
+#pragma unroll
+    for (int d = 0; d < 4; ++d) w[d] |= (e >> 3) == d ? c << sh : 0u;
+  };
+  if constexpr (P == 32) {
+    // a 32 x 32 first factor: rolled loops that form each value twice, since
+    // its 1024 values, loaded ahead by an unrolled loop, spill
+#pragma unroll 1
+    for (int i = 0; i < P; ++i) am = fmaxf(am, fabsf(out(i)));
+    sbyte = sbyte_of_amax(am);
+    scale = scale_of(sbyte);
+#pragma unroll 1
+    for (int i = 0; i < P; ++i) put(i, out(i));
+  } else {
+    float y[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      y[i] = out(i);
+      am = fmaxf(am, fabsf(y[i]));
+    }
+#pragma unroll
+    for (int o = 1; o < Q; o <<= 1) am = fmaxf(am, __shfl_xor(am, o));
+    sbyte = sbyte_of_amax(am);
+    scale = scale_of(sbyte);
+#pragma unroll
+    for (int i = 0; i < P; ++i) put(i, y[i]);
+  }
+#pragma unroll
+  for (int o = 1; o < Q; o <<= 1) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) w[d] |= (uint32_t)__shfl_xor((int)w[d], o);
+  }
+  if (k != 0) return;
+  const BlockOut o = block_out(a, row, b);
+  *reinterpret_cast<uint4*>(o.code) = make_uint4(w[0], w[1], w[2], w[3]);
+  *o.scale = (uint8_t)sbyte;
+}
+
+// OUT: 0 dense y (or none), 1 MXFP4.  ROT as in block_quant.h; P x Q the
+// Kronecker factors.  A row's d columns are at most 512 WPR EPL.
+template <int WPR, int EPL, bool VEC, int OUT, int ROT, int P, int Q>
+__global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_kernel(NormArgs a) {
+  // Kronecker: the row, 36 words per 32-element block
+  __shared__ __attribute__((aligned(16))) float krow[ROT == 2 ? 16 * WPR * EPL * 36 : 1];
+  __shared__ float slots[4 * WPR];
+  const int lane = threadIdx.x & 63;
+  const int wave = WPR == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t row = WPR == 1 ? blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : blockIdx.x;
+  if (WPR == 1 && row >= a.rows) return;
+  const uint32_t c0 = 8 * (lane + 64 * wave);
+  constexpr uint32_t STEP = 512 * WPR;
+  const int64_t voff = (a.gate != nullptr || a.scale != nullptr || a.shift != nullptr)
+                           ? (int64_t)(row / a.group_rows) * a.ld_vec
+                           : 0;
+
+  float v[EPL][8];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const uint32_t c = c0 + i * STEP;
+    if (c < a.d) load8<VEC>(a.x, a.x_bf16, (int64_t)row * a.ld_x, c, a.d, v[i]);
+    else
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+  }
+  if (a.post_norm) {
+    const float inv = statistics<EPL, WPR>(a, v, c0, slots, wave);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const uint32_t c = c0 + i * STEP;
+      if (c >= a.d) continue;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] *= inv;
+      if (a.post_weight != nullptr) {
+        float w[8];
+        load8<VEC>(a.post_weight, a.vec_bf16, 0, c, a.d, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] *= w[j];
+      }
+    }
+  }
+  if (a.gate != nullptr || a.residual != nullptr || a.residual_out != nullptr) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const uint32_t c = c0 + i * STEP;
+      if (c >= a.d) continue;
+      if (a.gate != nullptr) {
+        float w[8];
+        load8<VEC>(a.gate, a.vec_bf16, voff, c, a.d, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] *= w[j];
+      }
+      if (a.residual != nullptr) {
+        float w[8];
+        load8<VEC>(a.residual, a.r_bf16, (int64_t)row * a.ld_r, c, a.d, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = __builtin_fmaf(a.residual_scale, w[j], v[i][j]);
+      }
+      if (a.residual_out != nullptr) store8<VEC>(a.residual_out, a.r_bf16, (int64_t)row * a.ld_ro, c, a.d, v[i]);
+    }
+  }
+  if (OUT == 0 && a.y == nullptr) return;
+
+  const float inv = statistics<EPL, WPR>(a, v, c0, slots + 2 * WPR, wave);
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const uint32_t c = c0 + i * STEP;
+    // a lane past the row's end has no quad partner inside it (d % 32 == 0)
+    if (c < a.d) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] *= inv;
+      if (a.weight != nullptr) {
+        float w[8];
+        load8<VEC>(a.weight, a.vec_bf16, 0, c, a.d, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] *= w[j];
+      }
+      if (a.bias != nullptr) {
+        float w[8];
+        load8<VEC>(a.bias, a.vec_bf16, 0, c, a.d, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] += w[j];
+      }
+      if (a.scale != nullptr) {
+        float w[8];
+        load8<VEC>(a.scale, a.vec_bf16, voff, c, a.d, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] *= 1.0f + w[j];
+      }
+      if (a.shift != nullptr) {
+        float w[8];
+        load8<VEC>(a.shift, a.vec_bf16, voff, c, a.d, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] += w[j];
+      }
+    }
+    if constexpr (OUT == 0) {
+      if (c < a.d) store8<VEC>(a.y, a.y_bf16, (int64_t)row * a.ld_y, c, a.d, v[i]);
+    } else if constexpr (ROT != 2) {
+      if (c < a.d) quantize_quad<ROT>(a, v[i], row, c, lane);
+    } else {
+      if (c < a.d) {
+        float4* p = reinterpret_cast<float4*>(krow + (c >> 5) * 36 + (c & 31));
+        p[0] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+        p[1] = make_float4(v[i][4], v[i][5], v[i][6], v[i][7]);
+      }
+    }
+  }
+  if constexpr (OUT == 1 && ROT == 2) {
+    __syncthreads();
+    const uint32_t nblk = a.d >> 5;
+    constexpr uint32_t PER = 64 * WPR / Q;   // blocks a pass
+    for (uint32_t b0 = 0; b0 < nblk; b0 += PER) {
+      const uint32_t b = b0 + threadIdx.x / Q;
+      if (b < nblk) kron_block<P, Q>(a, krow + b * 36, row, b, lane % Q);   // whole groups of Q lanes
+    }
+  }
+}
+
+template <int WPR, int EPL, bool VEC, int OUT, int ROT, int P = 1, int Q = 32>
+void run(const NormArgs& a, hipStream_t s) {
+  const uint32_t grid = WPR == 1 ? (a.rows + 3) / 4 : a.rows;
+  norm_kernel<WPR, EPL, VEC, OUT, ROT, P, Q><<<grid, WPR == 1 ? 256 : 64 * WPR, 0, s>>>(a);
+}
+
+// A row's registers: 4 waves up to 16384 columns, 16 waves up to 65536.
+template <bool VEC, int OUT, int ROT>
+void run_width(const NormArgs& a, hipStream_t s) {
+  if (a.d <= 2048) run<4, 1, VEC, OUT, ROT>(a, s);
+  else if (a.d <= 4096) run<4, 2, VEC, OUT, ROT>(a, s);
+  else if (a.d <= 8192) run<4, 4, VEC, OUT, ROT>(a, s);
+  else if (a.d <= 16384) run<4, 8, VEC, OUT, ROT>(a, s);
+  else run<16, 8, VEC, OUT, ROT>(a, s);
+}
+
+template <int P, int Q>
+void run_kron(const NormArgs& a, hipStream_t s) {
+  if (a.d <= 4096) run<4, 2, true, 1, 2, P, Q>(a, s);
+  else run<4, 8, true, 1, 2, P, Q>(a, s);
+}
+
+hipError_t dispatch(const NormArgs& a, hipStream_t s) {
+  if (a.codes == nullptr) {
+    if (a.vec) run_width<true, 0, 0>(a, s);
+    else run_width<false, 0, 0>(a, s);
+    return hipGetLastError();
+  }
+  switch (a.rot) {
+    case 0: run_width<true, 1, 0>(a, s); break;
+    case 1: run_width<true, 1, 1>(a, s); break;
+    case 3: run_width<true, 1, 3>(a, s); break;
+    default:
+      switch (a.p) {
+        case 1: run_kron<1, 32>(a, s); break;
+        case 2: run_kron<2, 16>(a, s); break;
+        case 4: run_kron<4, 8>(a, s); break;
+        case 8: run_kron<8, 4>(a, s); break;
+        case 16: run_kron<16, 2>(a, s); break;
+        case 32: run_kron<32, 1>(a, s); break;
+        default: return hipErrorInvalidValue;
+      }
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
+  return dispatch(a, s);
+}
+
+}  // namespace mxfp4
