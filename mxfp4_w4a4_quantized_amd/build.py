@@ -20,7 +20,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmxfp4.so")
 CEILING_LIB = os.path.join(HERE, "libmxfp4_ceiling.so")
 SOURCES = ["api.cpp", "api_ffn.cpp", "quantize.hip", "gemm.hip", "gemm_large.hip", "gemm_small.hip",
-           "gemm_fused_small.hip", "norm.hip"]
+           "gemm_fused_small.hip", "gemm_fused_large.hip", "gemm_glu_large.hip",
+           "gemm_residual_large.hip", "norm.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

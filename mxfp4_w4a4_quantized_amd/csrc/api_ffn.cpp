@@ -131,9 +131,12 @@ mxfp4_status packed_output(const Rot& r, uint8_t* y_codes, uint8_t* y_scales, in
 }
 
 mxfp4_status launch_fused(const mxfp4::FusedArgs& f, void* stream) {
-  // one grid row per 64 rows of Y
-  if ((f.g.m + 63) / 64 > 65535) return MXFP4_ERR_UNSUPPORTED;
-  return from_hip(mxfp4::launch_fused_small(f, static_cast<hipStream_t>(stream)));
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  switch (mxfp4::fused_route(f)) {
+    case mxfp4::FusedRoute::kSmall: return from_hip(mxfp4::launch_fused_small(f, s));
+    case mxfp4::FusedRoute::kLarge: return from_hip(mxfp4::launch_fused_large(f, s));
+    default: return MXFP4_ERR_UNSUPPORTED;
+  }
 }
 
 // act, the vectors and their types of an epilogue (NULL: none)
