@@ -21,7 +21,8 @@ from typing import Optional
 
 import torch
 
-from . import (ROWMAJOR, RotationDesc, _check, _dtype_code, _on_device, _out_shapes, _rot_desc, _stream, lib)
+from . import (HADAMARD32, MXFP4_BF16, MXFP4_F32, ROT_HADAMARD32, ROWMAJOR, RotationDesc, _check, _out_shapes,
+               _rot_desc, lib)
 
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 NORM_KINDS = {"rms": 0, "layer": 1}
@@ -48,6 +49,12 @@ class GluDesc(ctypes.Structure):
     _fields_ = [("act", ctypes.c_int32), ("vec_dtype", ctypes.c_int32), ("g_codes", ctypes.c_void_p),
                 ("g_scales", ctypes.c_void_p), ("u_codes", ctypes.c_void_p), ("u_scales", ctypes.c_void_p),
                 ("bias_g", ctypes.c_void_p), ("bias_u", ctypes.c_void_p), ("reserved", ctypes.c_int32)]
+
+
+# The hipStream_t of a GPU's current stream.  torch.cuda.current_stream(dev)
+# .cuda_stream gives the same through a Stream object, which costs 1.7 us more
+# on each call.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def declare(L):
@@ -97,31 +104,65 @@ class Epilogue:
     residual: Optional[torch.Tensor] = None
 
 
-def _vec(name, t, shape, dtype, device):
-    """Checks a vector (or [groups, d] tensor) and gives (pointer, dtype of the call's vectors)."""
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device} (all operands on one GPU)")
+# The checks below run on every call of a decode step, whose kernels take a few
+# microseconds: they use the cheap tensor accessors (get_device, stride) and
+# fill each descriptor with one constructor call.
+
+
+def _bad(name, t, shape, dev):
+    """Why tensor t was refused."""
+    if t.get_device() != dev:
+        where = "the host" if t.get_device() < 0 else f"GPU {t.get_device()}"
+        return ValueError(f"{name} is on {where}, expected GPU {dev} (all operands on one GPU)")
     if t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if t.stride(-1) != 1 and t.shape[-1] != 1:
-        raise ValueError(f"{name} must have unit column stride")
+        return ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    return ValueError(f"{name} must have unit column stride")
+
+
+def _vec(name, t, shape, dtype, dev):
+    """Checks a vector and gives (pointer, dtype of the call's vectors)."""
+    if t.get_device() != dev or t.shape != shape or (t.stride() != (1,) and shape[0] != 1):
+        raise _bad(name, t, shape, dev)
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} is {t.dtype}, expected {dtype} (the vectors of a call share a dtype)")
     return t.data_ptr(), t.dtype
 
 
-def _matrix(name, t, shape, device):
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device} (all operands on one GPU)")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if t.stride(1) != 1 and t.shape[1] != 1:
-        raise ValueError(f"{name} must have unit column stride")
+def _matrix(name, t, shape, dev):
+    """Checks a dense matrix and gives (pointer, row stride: its width where
+    it has one row)."""
+    if t.get_device() != dev or t.shape != shape:
+        raise _bad(name, t, shape, dev)
+    ld, col = t.stride()
+    rows, cols = shape
+    if col != 1 and cols != 1:
+        raise _bad(name, t, shape, dev)
+    return t.data_ptr(), ld if rows > 1 or ld > cols else cols
 
 
-def _ld(t):
-    """Row stride of a matrix (its width where it has one row)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+def _grouped(name, t, shape, dtype, dev):
+    """Checks a [groups, d] tensor of vectors: (pointer, dtype, row stride)."""
+    ptr, ld = _matrix(name, t, shape, dev)
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} is {t.dtype}, expected {dtype} (the vectors of a call share a dtype)")
+    return ptr, t.dtype, ld
+
+
+_CODES = {torch.float32: MXFP4_F32, torch.bfloat16: MXFP4_BF16}
+
+
+def _code(dtype):
+    if dtype not in _CODES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    return _CODES[dtype]
+
+
+def _gpu(t):
+    """The GPU that a call's first operand is on."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"tensors must be on a GPU, got {t.device}")
+    return dev
 
 
 def _act_code(act):
@@ -137,86 +178,96 @@ def _groups(rows, group_rows, what):
 
 
 def _norm_desc(x, p, residual, residual_out):
-    if x.dim() != 2 or (x.stride(1) != 1 and x.shape[1] != 1):
+    """(descriptor, residual_out or the new tensor for it, GPU)"""
+    if x.dim() != 2:
         raise ValueError("x must be 2-D with unit column stride")
     if p.kind not in NORM_KINDS:
         raise ValueError(f"unknown norm {p.kind!r} (one of {', '.join(NORM_KINDS)})")
     if p.post_weight is not None and not p.post_norm:
         raise ValueError("post_weight needs post_norm")
-    device = x.device
-    _on_device(device)
-    rows, d = x.shape
-    d_ = NormDesc()
-    d_.kind, d_.x_dtype, d_.rows, d_.d = NORM_KINDS[p.kind], _dtype_code(x.dtype), rows, d
-    d_.x, d_.ld_x = x.data_ptr(), _ld(x)
-    changed = residual is not None or p.gate is not None or p.post_norm or residual_out is not None
+    dev = _gpu(x)
+    shape = x.shape
+    rows, d = shape
+    xp, ld_x = _matrix("x", x, shape, dev)
+    res, ld_r, out, ld_ro, rt = None, 0, None, 0, 0
     if residual is not None:
-        _matrix("residual", residual, x.shape, device)
-        d_.residual, d_.ld_r = residual.data_ptr(), _ld(residual)
-    if changed:
+        res, ld_r = _matrix("residual", residual, shape, dev)
+    if residual is not None or residual_out is not None or p.gate is not None or p.post_norm:
+        like = x if residual is None else residual
         if residual_out is None:
-            residual_out = torch.empty_like(x if residual is None else residual, memory_format=torch.contiguous_format)
-        else:
-            _matrix("residual_out", residual_out, x.shape, device)
-            if residual is not None and residual_out.dtype != residual.dtype:
-                raise ValueError(f"residual_out is {residual_out.dtype}, residual {residual.dtype}")
-        d_.residual_out, d_.ld_ro = residual_out.data_ptr(), _ld(residual_out)
-        d_.r_dtype = _dtype_code(residual_out.dtype)
-    dtype = None
-    for name in ("post_weight", "weight", "bias"):
-        t = getattr(p, name)
-        if t is not None:
-            ptr, dtype = _vec(name, t, (d,), dtype, device)
-            setattr(d_, name, ptr)
-    ld_vec = None
-    for name in ("gate", "scale", "shift"):
-        t = getattr(p, name)
-        if t is not None:
-            ptr, dtype = _vec(name, t, (_groups(rows, p.group_rows, name), d), dtype, device)
-            setattr(d_, name, ptr)
-            if ld_vec is not None and _ld(t) != ld_vec and t.shape[0] > 1:
-                raise ValueError("gate, scale and shift must have the same row stride")
-            ld_vec = _ld(t)
-    if ld_vec is not None:
-        d_.ld_vec, d_.group_rows = ld_vec, p.group_rows
-    if dtype is not None:
-        d_.vec_dtype = _dtype_code(dtype)
-    d_.residual_scale, d_.eps, d_.post_norm = p.residual_scale, p.eps, int(p.post_norm)
-    return d_, residual_out if changed else None
+            residual_out = torch.empty_like(like)
+        elif residual is not None and residual_out.dtype != residual.dtype:
+            raise ValueError(f"residual_out is {residual_out.dtype}, residual {residual.dtype}")
+        out, ld_ro = _matrix("residual_out", residual_out, shape, dev)
+        rt = _code(residual_out.dtype)
+    dtype, post, weight, bias, gate, scale, shift, ld_vec = None, None, None, None, None, None, None, 0
+    if p.post_weight is not None:
+        post, dtype = _vec("post_weight", p.post_weight, (d,), dtype, dev)
+    if p.weight is not None:
+        weight, dtype = _vec("weight", p.weight, (d,), dtype, dev)
+    if p.bias is not None:
+        bias, dtype = _vec("bias", p.bias, (d,), dtype, dev)
+    if p.gate is not None or p.scale is not None or p.shift is not None:
+        vshape = (_groups(rows, p.group_rows, "a grouped vector"), d)
+        lds = set()
+        if p.gate is not None:
+            gate, dtype, ld = _grouped("gate", p.gate, vshape, dtype, dev)
+            lds.add(ld)
+        if p.scale is not None:
+            scale, dtype, ld = _grouped("scale", p.scale, vshape, dtype, dev)
+            lds.add(ld)
+        if p.shift is not None:
+            shift, dtype, ld = _grouped("shift", p.shift, vshape, dtype, dev)
+            lds.add(ld)
+        if len(lds) > 1 and vshape[0] > 1:
+            raise ValueError("gate, scale and shift must have the same row stride")
+        ld_vec = max(lds)
+    desc = NormDesc(NORM_KINDS[p.kind], _code(x.dtype), rt, 0 if dtype is None else _code(dtype), rows, d, xp, ld_x,
+                    res, ld_r, out, ld_ro, post, weight, bias, gate, scale, shift, ld_vec, p.group_rows,
+                    p.residual_scale, p.eps, 1 if p.post_norm else 0, 0)
+    return desc, residual_out, dev
 
 
 def norm(x, p: Norm, residual=None, out_dtype=None, y=None, residual_out=None):
     """Returns (y, r): the norm of r (dense, x's dtype by default) and the new
     residual stream r (residual's dtype; None where r is x itself).
     residual_out may be `residual`, which then holds r."""
-    desc, r = _norm_desc(x, p, residual, residual_out)
+    desc, r, dev = _norm_desc(x, p, residual, residual_out)
     if y is None:
-        y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-    else:
-        _matrix("y", y, x.shape, x.device)
-    _check(lib().mxfp4_norm(ctypes.byref(desc), y.data_ptr(), _dtype_code(y.dtype), _ld(y), _stream(x.device)),
-           "mxfp4_norm")
+        y = torch.empty_like(x, dtype=out_dtype)
+    ptr, ld = _matrix("y", y, x.shape, dev)
+    _check(lib().mxfp4_norm(desc, ptr, _code(y.dtype), ld, _raw_stream(dev)), "mxfp4_norm")
     return y, r
 
 
-def _packed_outputs(rows, k, layout, codes, scales, device):
+def _packed(name, codes, scales, rows, k, layout, dev):
+    """Checks packed codes and scales of [rows, k] in `layout`: (pointers)"""
     cshape, sshape = _out_shapes(rows, k, layout)
-    if codes is None:
-        codes = torch.empty(cshape, dtype=torch.uint8, device=device)
-    if scales is None:
-        scales = torch.empty(sshape, dtype=torch.uint8, device=device)
-    _packed("output", codes, scales, cshape, sshape, device)
-    return codes, scales
+    if (codes.shape != cshape or scales.shape != sshape or codes.get_device() != dev or scales.get_device() != dev or
+            codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not codes.is_contiguous() or
+            not scales.is_contiguous()):
+        for t in (codes, scales):
+            if t.get_device() != dev:
+                raise _bad(f"{name} codes/scales", t, t.shape, dev)
+        if codes.shape != cshape or scales.shape != sshape:
+            raise ValueError(f"{name}: codes/scales must be {cshape} / {sshape}")
+        raise ValueError(f"{name}: codes and scales must be contiguous uint8 tensors")
+    return codes.data_ptr(), scales.data_ptr()
 
 
-def _packed(name, codes, scales, cshape, sshape, device):
-    for t, shape in ((codes, cshape), (scales, sshape)):
-        if t.device != device:
-            raise ValueError(f"{name} codes/scales are on {t.device}, expected {device} (all operands on one GPU)")
-        if t.shape != shape:
-            raise ValueError(f"{name} codes/scales must be {cshape} / {sshape}")
-        if t.dtype != torch.uint8 or not t.is_contiguous():
-            raise ValueError(f"{name} codes and scales must be contiguous uint8 tensors")
+def _packed_outputs(rows, k, layout, codes, scales, like):
+    """Codes and scales for a packed result (new ones beside tensor `like`
+    where not given) and their pointers."""
+    if codes is None or scales is None:
+        cshape, sshape = _out_shapes(rows, k, layout)
+        new = codes is None and scales is None
+        if codes is None:
+            codes = torch.empty(cshape, dtype=torch.uint8, device=like.device)
+        if scales is None:
+            scales = torch.empty(sshape, dtype=torch.uint8, device=like.device)
+        if new:
+            return codes, scales, codes.data_ptr(), scales.data_ptr()
+    return codes, scales, *_packed("output", codes, scales, rows, k, layout, like.get_device())
 
 
 def norm_quantize(x, p: Norm, residual=None, rot=None, layout: int = ROWMAJOR, codes=None, scales=None,
@@ -224,108 +275,104 @@ def norm_quantize(x, p: Norm, residual=None, rot=None, layout: int = ROWMAJOR, c
     """Returns (codes, scales, r): the norm quantized to MXFP4 in `layout`
     after the block transform `rot` (the bytes that quantize_rotate gives for
     the fp32 y of norm()), and r as norm() returns it."""
-    desc, r = _norm_desc(x, p, residual, residual_out)
+    desc, r, dev = _norm_desc(x, p, residual, residual_out)
     rows, d = x.shape
-    codes, scales = _packed_outputs(rows, d, layout, codes, scales, x.device)
-    rdesc, _keep = _rot_desc(rot, x.device, d)
-    _check(lib().mxfp4_norm_quantize(ctypes.byref(desc), ctypes.byref(rdesc) if rdesc is not None else None, layout,
-                                     codes.data_ptr(), scales.data_ptr(), _stream(x.device)), "mxfp4_norm_quantize")
+    codes, scales, cp, sp = _packed_outputs(rows, d, layout, codes, scales, x)
+    rdesc, _keep = _rotation(rot, x, d)
+    _check(lib().mxfp4_norm_quantize(desc, rdesc, layout, cp, sp, _raw_stream(dev)), "mxfp4_norm_quantize")
     return codes, scales, r
 
 
-def _operand_sizes(a_codes, a_scales, weights, layout, m, n):
-    """Checks the packed operands; gives (m, n, k).  For TILED operands pass
-    the real row counts."""
-    device = a_codes.device
-    _on_device(device)
-    k = a_codes.shape[1] * 2
-    m = a_codes.shape[0] if m is None else m
-    n = weights[0][0].shape[0] if n is None else n
-    _packed("operand A:", a_codes, a_scales, *_out_shapes(m, k, layout), device)
-    shapes = _out_shapes(n, k, layout)
-    for c, s in weights:
-        _packed("weight:", c, s, *shapes, device)
-    return m, n, k
+_H32 = RotationDesc(ROT_HADAMARD32, 0, 0, 0, None, None)
 
 
-def _dense_output(y, m, n, out_dtype, device):
+def _rotation(rot, like, k):
+    """Rotation descriptor and the factor tensors it points to."""
+    if rot is None:
+        return None, ()
+    return (_H32, ()) if rot == HADAMARD32 else _rot_desc(rot, like.device, k)
+
+
+def _sizes(a_codes, b_codes, m, n):
+    """(m, n, k): for TILED operands the caller passes the real row counts."""
+    return (a_codes.shape[0] if m is None else m, b_codes.shape[0] if n is None else n, a_codes.shape[1] * 2)
+
+
+def _dense_output(y, m, n, out_dtype, like):
+    """(y, its pointer, its row stride, its dtype code)"""
     if y is None:
-        return torch.empty((m, n), dtype=out_dtype, device=device)
-    _matrix("y", y, (m, n), device)
-    return y
+        y = torch.empty((m, n), dtype=out_dtype, device=like.device)
+        return y, y.data_ptr(), n, _code(out_dtype)
+    ptr, ld = _matrix("y", y, (m, n), like.get_device())
+    return y, ptr, ld, _code(y.dtype)
 
 
-def _epilogue_desc(e, m, n, device):
-    d = EpilogueDesc()
+def _epilogue_desc(e, m, n, dev):
     if e is None:
-        return d
-    d.act = _act_code(e.act)
-    dtype = None
+        return None
+    bias, gate, ld_gate, res, ld_res, rt, dtype = None, None, 0, None, 0, 0, None
     if e.bias is not None:
-        d.bias, dtype = _vec("bias", e.bias, (n,), dtype, device)
+        bias, dtype = _vec("bias", e.bias, (n,), dtype, dev)
     if e.gate is not None:
-        d.gate, dtype = _vec("gate", e.gate, (_groups(m, e.group_rows, "gate"), n), dtype, device)
-        d.ld_gate, d.group_rows = _ld(e.gate), e.group_rows
-    if dtype is not None:
-        d.vec_dtype = _dtype_code(dtype)
+        gate, dtype, ld_gate = _grouped("gate", e.gate, (_groups(m, e.group_rows, "gate"), n), dtype, dev)
     if e.residual is not None:
-        _matrix("residual", e.residual, (m, n), device)
-        d.residual, d.ld_res, d.res_dtype = e.residual.data_ptr(), _ld(e.residual), _dtype_code(e.residual.dtype)
-    return d
+        res, ld_res = _matrix("residual", e.residual, (m, n), dev)
+        rt = _code(e.residual.dtype)
+    return EpilogueDesc(_act_code(e.act), 0 if dtype is None else _code(dtype), bias, gate, ld_gate,
+                        e.group_rows, res, ld_res, rt, 0)
 
 
 def gemm_epilogue(a_codes, a_scales, b_codes, b_scales, e: Epilogue = None, out_dtype=torch.bfloat16, y=None,
                   layout: int = ROWMAJOR, m: int = None, n: int = None):
     """Y = residual + gate * act(A B^T + bias) on packed MXFP4 operands, fp32
     throughout, rounded once to fp32 or bf16 Y [m, n]."""
-    m, n, k = _operand_sizes(a_codes, a_scales, ((b_codes, b_scales),), layout, m, n)
-    device = a_codes.device
-    desc = _epilogue_desc(e, m, n, device)
-    y = _dense_output(y, m, n, out_dtype, device)
-    _check(lib().mxfp4_gemm_epilogue(a_codes.data_ptr(), a_scales.data_ptr(), m, b_codes.data_ptr(),
-                                     b_scales.data_ptr(), n, k, layout, ctypes.byref(desc), y.data_ptr(),
-                                     _dtype_code(y.dtype), _ld(y), _stream(device)), "mxfp4_gemm_epilogue")
+    dev = _gpu(a_codes)
+    m, n, k = _sizes(a_codes, b_codes, m, n)
+    ac, as_ = _packed("operand A", a_codes, a_scales, m, k, layout, dev)
+    bc, bs = _packed("operand B", b_codes, b_scales, n, k, layout, dev)
+    desc = _epilogue_desc(e, m, n, dev)
+    y, ptr, ld, yt = _dense_output(y, m, n, out_dtype, a_codes)
+    _check(lib().mxfp4_gemm_epilogue(ac, as_, m, bc, bs, n, k, layout, desc, ptr, yt, ld, _raw_stream(dev)),
+           "mxfp4_gemm_epilogue")
     return y
 
 
 def gemm_epilogue_requant(a_codes, a_scales, b_codes, b_scales, e: Epilogue = None, rot=None, layout: int = ROWMAJOR,
                           out_layout: int = ROWMAJOR, m: int = None, n: int = None, y_codes=None, y_scales=None):
     """(codes, scales) of rot(act(A B^T + bias)) in `out_layout`; rot None or "h32"."""
-    m, n, k = _operand_sizes(a_codes, a_scales, ((b_codes, b_scales),), layout, m, n)
-    device = a_codes.device
-    desc = _epilogue_desc(e, m, n, device)
-    rdesc, _keep = _rot_desc(rot, device, n)
-    y_codes, y_scales = _packed_outputs(m, n, out_layout, y_codes, y_scales, device)
-    _check(lib().mxfp4_gemm_epilogue_requant(
-        a_codes.data_ptr(), a_scales.data_ptr(), m, b_codes.data_ptr(), b_scales.data_ptr(), n, k, layout,
-        ctypes.byref(desc), ctypes.byref(rdesc) if rdesc is not None else None, y_codes.data_ptr(),
-        y_scales.data_ptr(), out_layout, _stream(device)), "mxfp4_gemm_epilogue_requant")
+    dev = _gpu(a_codes)
+    m, n, k = _sizes(a_codes, b_codes, m, n)
+    ac, as_ = _packed("operand A", a_codes, a_scales, m, k, layout, dev)
+    bc, bs = _packed("operand B", b_codes, b_scales, n, k, layout, dev)
+    desc = _epilogue_desc(e, m, n, dev)
+    rdesc, _keep = _rotation(rot, a_codes, n)
+    y_codes, y_scales, yc, ys = _packed_outputs(m, n, out_layout, y_codes, y_scales, a_codes)
+    _check(lib().mxfp4_gemm_epilogue_requant(ac, as_, m, bc, bs, n, k, layout, desc, rdesc, yc, ys, out_layout,
+                                             _raw_stream(dev)), "mxfp4_gemm_epilogue_requant")
     return y_codes, y_scales
 
 
-def _glu_desc(act, g, u, bias_g, bias_u, n, device):
-    d = GluDesc(act=_act_code(act), g_codes=g[0].data_ptr(), g_scales=g[1].data_ptr(), u_codes=u[0].data_ptr(),
-                u_scales=u[1].data_ptr())
-    dtype = None
+def _glu_desc(act, g_codes, g_scales, u_codes, u_scales, bias_g, bias_u, n, k, layout, dev):
+    gc, gs = _packed("weight G", g_codes, g_scales, n, k, layout, dev)
+    uc, us = _packed("weight U", u_codes, u_scales, n, k, layout, dev)
+    bg, bu, dtype = None, None, None
     if bias_g is not None:
-        d.bias_g, dtype = _vec("bias_g", bias_g, (n,), dtype, device)
+        bg, dtype = _vec("bias_g", bias_g, (n,), dtype, dev)
     if bias_u is not None:
-        d.bias_u, dtype = _vec("bias_u", bias_u, (n,), dtype, device)
-    if dtype is not None:
-        d.vec_dtype = _dtype_code(dtype)
-    return d
+        bu, dtype = _vec("bias_u", bias_u, (n,), dtype, dev)
+    return GluDesc(_act_code(act), 0 if dtype is None else _code(dtype), gc, gs, uc, us, bg, bu, 0)
 
 
 def gemm_glu(a_codes, a_scales, g_codes, g_scales, u_codes, u_scales, act="silu", bias_g=None, bias_u=None,
              out_dtype=torch.bfloat16, y=None, layout: int = ROWMAJOR, m: int = None, n: int = None):
     """H = act(A G^T + bias_g) * (A U^T + bias_u) in one kernel: G and U the
     gate and up projections' packed weights, n rows each."""
-    m, n, k = _operand_sizes(a_codes, a_scales, ((g_codes, g_scales), (u_codes, u_scales)), layout, m, n)
-    device = a_codes.device
-    desc = _glu_desc(act, (g_codes, g_scales), (u_codes, u_scales), bias_g, bias_u, n, device)
-    y = _dense_output(y, m, n, out_dtype, device)
-    _check(lib().mxfp4_gemm_glu(a_codes.data_ptr(), a_scales.data_ptr(), m, ctypes.byref(desc), n, k, layout,
-                                y.data_ptr(), _dtype_code(y.dtype), _ld(y), _stream(device)), "mxfp4_gemm_glu")
+    dev = _gpu(a_codes)
+    m, n, k = _sizes(a_codes, g_codes, m, n)
+    ac, as_ = _packed("operand A", a_codes, a_scales, m, k, layout, dev)
+    desc = _glu_desc(act, g_codes, g_scales, u_codes, u_scales, bias_g, bias_u, n, k, layout, dev)
+    y, ptr, ld, yt = _dense_output(y, m, n, out_dtype, a_codes)
+    _check(lib().mxfp4_gemm_glu(ac, as_, m, desc, n, k, layout, ptr, yt, ld, _raw_stream(dev)), "mxfp4_gemm_glu")
     return y
 
 
@@ -333,15 +380,14 @@ def gemm_glu_requant(a_codes, a_scales, g_codes, g_scales, u_codes, u_scales, ac
                      rot=None, layout: int = ROWMAJOR, out_layout: int = ROWMAJOR, m: int = None, n: int = None,
                      y_codes=None, y_scales=None):
     """(codes, scales) of rot(act(A G^T + bias_g) * (A U^T + bias_u)); rot None or "h32"."""
-    m, n, k = _operand_sizes(a_codes, a_scales, ((g_codes, g_scales), (u_codes, u_scales)), layout, m, n)
-    device = a_codes.device
-    desc = _glu_desc(act, (g_codes, g_scales), (u_codes, u_scales), bias_g, bias_u, n, device)
-    rdesc, _keep = _rot_desc(rot, device, n)
-    y_codes, y_scales = _packed_outputs(m, n, out_layout, y_codes, y_scales, device)
-    _check(lib().mxfp4_gemm_glu_requant(
-        a_codes.data_ptr(), a_scales.data_ptr(), m, ctypes.byref(desc), n, k, layout,
-        ctypes.byref(rdesc) if rdesc is not None else None, y_codes.data_ptr(), y_scales.data_ptr(), out_layout,
-        _stream(device)), "mxfp4_gemm_glu_requant")
+    dev = _gpu(a_codes)
+    m, n, k = _sizes(a_codes, g_codes, m, n)
+    ac, as_ = _packed("operand A", a_codes, a_scales, m, k, layout, dev)
+    desc = _glu_desc(act, g_codes, g_scales, u_codes, u_scales, bias_g, bias_u, n, k, layout, dev)
+    rdesc, _keep = _rotation(rot, a_codes, n)
+    y_codes, y_scales, yc, ys = _packed_outputs(m, n, out_layout, y_codes, y_scales, a_codes)
+    _check(lib().mxfp4_gemm_glu_requant(ac, as_, m, desc, n, k, layout, rdesc, yc, ys, out_layout, _raw_stream(dev)),
+           "mxfp4_gemm_glu_requant")
     return y_codes, y_scales
 
 
