@@ -44,17 +44,5 @@ __device__ __forceinline__ float gelu(float x) {
   return x * (x < 0.0f ? q : 1.0f - q);
 }
 
-// act chosen at run time (uniform over the grid): the small-M kernels, whose
-// time is the weight stream.
-__device__ __forceinline__ float any(int kind, float x) {
-  switch (kind) {
-    case RELU: return relu(x);
-    case SILU: return silu(x);
-    case GELU: return gelu(x);
-    case GELU_TANH: return gelu_tanh(x);
-    default: return x;
-  }
-}
-
 }  // namespace act
 }  // namespace mxfp4

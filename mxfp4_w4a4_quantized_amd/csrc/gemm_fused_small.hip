@@ -15,55 +15,186 @@
 #include "gemm_small_core.h"
 #include "activation.h"
 
+#include <type_traits>
+
 namespace mxfp4 {
 namespace {
 
 using namespace smallm;
 
-__device__ __forceinline__ float elem(const void* p, bool bf16, int64_t i) {
-  if (bf16) return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
-  return static_cast<const float*>(p)[i];
+// Tiled operands: the scale bytes of one K step of a 16-row fragment are 64
+// contiguous bytes (row-major [16][4]).  Lane (r, g) loads the dword of row r
+// for step s0 + 4 i + g, i.e. the scales of all four blocks of that step; the
+// scale of step s0 + 4 i + j for the lane's own block g then sits in byte g of
+// lane (r, j)'s dword.  One dword load replaces four byte loads.  Steps past
+// `last` read its dword (never used).
+template <int NCH>
+__device__ __forceinline__ void chunk_scales(const Operand& o, int s0, int last, int lane, int (&sc)[NCH]) {
+  const int lr = lane & 15, lg = lane >> 4;
+#pragma unroll
+  for (int i = 0; i < NCH / 4; ++i) {
+    const int dw = *reinterpret_cast<const int*>(o.scale_row + (int64_t)min(s0 + 4 * i + lg, last) * o.sstride);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sc[4 * i + j] = __shfl(dw, 16 * j + lr) >> (8 * lg);
+  }
 }
 
-// What the epilogue of one lane's four columns reads.
+// One chunk of NCH steps from s0 on into the accumulator tiles.  FULL: every
+// step lies inside the wave's range and inside K; the loads have no predicates
+// and constant offsets.  Otherwise steps from s_end on are left out: tiled
+// operands (no K tail inside a step) load the last step again in their place,
+// row-major ones take predicated loads, which also cover blocks past K.
+template <int MG, int NG, bool TILED, int NCH, bool FULL>
+__device__ __forceinline__ void k_chunk(const Operand (&w)[NG], const Operand (&x)[MG], v4f (&acc)[NG][MG], int s0,
+                                        int s_end, int kblocks, int lane) {
+  const int lg = lane >> 4;
+  const int last = s_end - 1;
+  auto load = [&](const Operand& o, int j, auto stream, u32x4& code, int& scale) {
+    const int s = TILED && !FULL ? min(s0 + j, last) : s0 + j;
+    if (FULL || TILED || (s < s_end && 4 * s + lg < kblocks)) {
+      const u32x4* p = reinterpret_cast<const u32x4*>(o.code + s * o.cstride);
+      if constexpr (decltype(stream)::value) code = __builtin_nontemporal_load(p);
+      else code = *p;
+      if constexpr (!TILED) scale = o.scale[s * o.sstride];
+    } else {
+      code = u32x4{0u, 0u, 0u, 0u};
+      scale = 0;
+    }
+  };
+  u32x4 wf[NG][NCH];
+  int ws[NG][NCH];
+#pragma unroll
+  for (int j = 0; j < NCH; ++j)
+#pragma unroll
+    for (int q = 0; q < NG; ++q) load(w[q], j, std::true_type{}, wf[q][j], ws[q][j]);
+  if constexpr (TILED) {
+#pragma unroll
+    for (int q = 0; q < NG; ++q) chunk_scales<NCH>(w[q], s0, last, lane, ws[q]);
+  }
+  // the next M group's activations load while this one's MFMAs run (not with
+  // 4 x 4 accumulator tiles: no registers for it)
+  constexpr int NB = MG * NG < 16 ? 2 : 1;
+  u32x4 xf[NB][NCH];
+  int xs[NB][NCH];
+  auto load_x = [&](int mg) {
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) load(x[mg], j, std::false_type{}, xf[mg % NB][j], xs[mg % NB][j]);
+    if constexpr (TILED) chunk_scales<NCH>(x[mg], s0, last, lane, xs[mg % NB]);
+  };
+  load_x(0);
+#pragma unroll
+  for (int mg = 0; mg < MG; ++mg) {
+    if (NB == 2 ? mg + 1 < MG : mg > 0) load_x(NB == 2 ? mg + 1 : mg);
+    // in this order: left to itself the compiler moves the next group's loads
+    // behind these MFMAs (64 rows x 4096 -> 2 x 14336: 20.9 instead of 19.5 us)
+    if constexpr (MG > 1) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < NCH; ++j)
+      if (FULL || s0 + j < s_end) {
+#pragma unroll
+        for (int q = 0; q < NG; ++q) acc[q][mg] = mma(wf[q][j], xf[mg % NB][j], acc[q][mg], ws[q][j], xs[mg % NB][j]);
+      }
+  }
+}
+
+// One wave's K range [s_begin, s_end): NG weight fragments against MG
+// activation fragments per step, the steps in ascending order whatever the
+// chunk length NCH, so that every kernel that takes the same split forms the
+// same sums.
+template <int MG, int NG, bool TILED, int NCH>
+__device__ __forceinline__ void k_loop(const Operand (&w)[NG], const Operand (&x)[MG], v4f (&acc)[NG][MG], int s_begin,
+                                       int s_end, int kblocks, int lane) {
+  int s0 = s_begin;
+  for (; s0 + NCH <= s_end && (TILED || 4 * (s0 + NCH) <= kblocks); s0 += NCH)
+    k_chunk<MG, NG, TILED, NCH, true>(w, x, acc, s0, s_end, kblocks, lane);
+  for (; s0 < s_end; s0 += NCH) k_chunk<MG, NG, TILED, NCH, false>(w, x, acc, s0, s_end, kblocks, lane);
+}
+
+// Four elements from index i on, of which the first `left` are in range (the
+// others repeat the last one: no predicates).
+__device__ __forceinline__ v4f load4(const void* p, bool bf16, int64_t i, int left) {
+  v4f v;
+  if (bf16) {
+    const uint16_t* q = static_cast<const uint16_t*>(p) + i;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = __uint_as_float((uint32_t)q[min(r, left - 1)] << 16);
+  } else {
+    const float* q = static_cast<const float*>(p) + i;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = q[min(r, left - 1)];
+  }
+  return v;
+}
+
+// What the epilogue of one lane's four columns reads.  Rows and columns past
+// the end read the last ones (their results are not stored).
+template <bool GLU>
 struct Extra {
-  v4f bias, bias_u, gate, res;
+  v4f bias, bias_u;
+};
+template <>
+struct Extra<false> {
+  v4f bias, gate, res;
 };
 
 template <bool GLU>
-__device__ __forceinline__ void load_extra(const FusedArgs& f, int m, int n, Extra& e) {
-  const bool row = m < f.g.m;
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const bool ok = n + r < f.g.n;
-    e.bias[r] = f.bias != nullptr && ok ? elem(f.bias, f.vec_bf16, n + r) : 0.0f;
-    if constexpr (GLU) {
-      e.bias_u[r] = f.bias_u != nullptr && ok ? elem(f.bias_u, f.vec_bf16, n + r) : 0.0f;
-    } else {
-      e.gate[r] = f.gate != nullptr && ok && row
-                      ? elem(f.gate, f.vec_bf16, (int64_t)((uint32_t)m / f.group_rows) * f.ld_gate + n + r)
-                      : 1.0f;
-      e.res[r] = f.residual != nullptr && ok && row ? elem(f.residual, f.res_bf16, (int64_t)m * f.ld_res + n + r) : 0.0f;
-    }
+__device__ __forceinline__ void load_extra(const FusedArgs& f, int m, int n, Extra<GLU>& e) {
+  m = min(m, f.g.m - 1);
+  n = min(n, f.g.n - 1);
+  const int left = f.g.n - n;
+  if (f.bias != nullptr) e.bias = load4(f.bias, f.vec_bf16, n, left);
+  if constexpr (GLU) {
+    if (f.bias_u != nullptr) e.bias_u = load4(f.bias_u, f.vec_bf16, n, left);
+  } else {
+    if (f.gate != nullptr)
+      e.gate = load4(f.gate, f.vec_bf16, (int64_t)((uint32_t)m / f.group_rows) * f.ld_gate + n, left);
+    if (f.residual != nullptr) e.res = load4(f.residual, f.res_bf16, (int64_t)m * f.ld_res + n, left);
   }
 }
 
-template <bool GLU>
-__device__ __forceinline__ v4f finish(const FusedArgs& f, const Extra& e, const v4f& v, const v4f& u) {
-  v4f y;
+// act on every value, chosen once
+template <int N>
+__device__ __forceinline__ void activate(int kind, v4f (&v)[N]) {
+  auto apply = [&](auto fn) __attribute__((always_inline)) {
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const float b = f.bias != nullptr ? v[r] + e.bias[r] : v[r];
-    float a = act::any(f.act, b);
-    if constexpr (GLU) {
-      a *= f.bias_u != nullptr ? u[r] + e.bias_u[r] : u[r];
-    } else {
-      if (f.gate != nullptr) a *= e.gate[r];
-      if (f.residual != nullptr) a += e.res[r];
-    }
-    y[r] = a;
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[i][r] = fn(v[i][r]);
+  };
+  switch (kind) {
+    case act::RELU: apply([](float x) __attribute__((always_inline)) { return act::relu(x); }); break;
+    case act::SILU: apply([](float x) __attribute__((always_inline)) { return act::silu(x); }); break;
+    case act::GELU: apply([](float x) __attribute__((always_inline)) { return act::gelu(x); }); break;
+    case act::GELU_TANH: apply([](float x) __attribute__((always_inline)) { return act::gelu_tanh(x); }); break;
+    default: break;
   }
-  return y;
+}
+
+// The epilogue of N fragments of a lane: v their sums (u: the up projection's).
+template <bool GLU, int N>
+__device__ __forceinline__ void finish(const FusedArgs& f, const Extra<GLU> (&e)[N], v4f (&v)[N], v4f (&u)[N]) {
+  if (f.bias != nullptr) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += e[i].bias;
+  }
+  activate(f.act, v);
+  if constexpr (GLU) {
+    if (f.bias_u != nullptr) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) u[i] += e[i].bias_u;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] *= u[i];
+  } else {
+    if (f.gate != nullptr) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] *= e[i].gate;
+    }
+    if (f.residual != nullptr) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += e[i].res;
+    }
+  }
 }
 
 // Hadamard-32 of the 32-column block of each row: lane (r, g) holds columns
@@ -92,6 +223,31 @@ __device__ __forceinline__ void hadamard_lanes(v4f& v0, v4f& v1, int lane) {
     const float s = v0[r] + v1[r], d = v0[r] - v1[r];
     v0[r] = s * c;
     v1[r] = d * c;
+  }
+}
+
+// Y[m][n .. n + 3], bounds-checked against N.
+template <bool BF16>
+__device__ __forceinline__ void store4(const GemmArgs& g, int m, int n, const v4f& y, int y_vec) {
+  if constexpr (BF16) {
+    uint16_t* yp = static_cast<uint16_t*>(g.y) + (int64_t)m * g.ld_y + n;
+    const uint32_t d0 = pack_bf16(y[0], y[1]), d1 = pack_bf16(y[2], y[3]);
+    if (y_vec && n + 3 < g.n) {
+      *reinterpret_cast<uint2*>(yp) = make_uint2(d0, d1);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (n + r < g.n) yp[r] = (uint16_t)((r < 2 ? d0 : d1) >> (16 * (r & 1)));
+    }
+  } else {
+    float* yp = static_cast<float*>(g.y) + (int64_t)m * g.ld_y + n;
+    if (y_vec && n + 3 < g.n) {
+      *reinterpret_cast<float4*>(yp) = make_float4(y[0], y[1], y[2], y[3]);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (n + r < g.n) yp[r] = y[r];
+    }
   }
 }
 
@@ -130,6 +286,25 @@ __global__ __launch_bounds__(64 * MAXW) void gemm_fused_small_kernel(FusedArgs f
 #pragma unroll
     for (int mg = 0; mg < MG; ++mg) acc[q][mg] = v4f{0.f, 0.f, 0.f, 0.f};
 
+  // Output units over the waves: the two fragments of a row group's 32-block
+  // (MXFP4) or one fragment.  What the epilogue of this wave's first unit reads
+  // is loaded ahead of the K loop: behind it, it costs a round trip to HBM.
+  constexpr int UF = OUT == 2 ? 2 : 1, NU = MG * PG / UF;
+  auto unit = [&](int i, int h, int& p, int& mg) {
+    p = OUT == 2 ? h : i / MG;
+    mg = OUT == 2 ? i : i % MG;
+  };
+  Extra<GLU> e[UF];
+  auto load_unit = [&](int i) {
+#pragma unroll
+    for (int h = 0; h < UF; ++h) {
+      int p, mg;
+      unit(i, h, p, mg);
+      load_extra<GLU>(f, m0 + 16 * mg + lr, n0 + 16 * p + 4 * lg, e[h]);
+    }
+  };
+  if (wave < NU) load_unit(wave);
+
   k_loop<MG, NG, TILED, NCH>(w, x, acc, s_begin, s_end, g.k >> 5, lane);
 
 #pragma unroll
@@ -144,65 +319,69 @@ __global__ __launch_bounds__(64 * MAXW) void gemm_fused_small_kernel(FusedArgs f
     for (int w2 = 1; w2 < nwaves; ++w2) sum += red[w2][q * MG + mg][lane];
     return sum;
   };
-  auto output = [&](int p, int mg) {
-    const v4f v = total(p, mg);
-    v4f u = v;
-    if constexpr (GLU) u = total(PG + p, mg);
-    Extra e;
-    load_extra<GLU>(f, m0 + 16 * mg + lr, n0 + 16 * p + 4 * lg, e);
-    return finish<GLU>(f, e, v, u);
-  };
-  if constexpr (OUT == 2) {
-    for (int mg = wave; mg < MG; mg += nwaves) {
-      v4f h0 = output(0, mg), h1 = output(1, mg);
-      if (f.h32) hadamard_lanes(h0, h1, lane);
-      store_requant(g, m0 + 16 * mg + lr, n0, h0, h1, lane);
+  for (int i = wave; i < NU; i += nwaves) {
+    if (i != wave) load_unit(i);
+    v4f v[UF], u[UF];
+    int p, mg;
+#pragma unroll
+    for (int h = 0; h < UF; ++h) {
+      unit(i, h, p, mg);
+      v[h] = total(p, mg);
+      if constexpr (GLU) u[h] = total(PG + p, mg);
     }
-  } else {
-    for (int i = wave; i < MG * PG; i += nwaves) {
-      const int p = i / MG, mg = i % MG;
-      const v4f y = output(p, mg);
-      const int m = m0 + 16 * mg + lr, n = n0 + 16 * p + 4 * lg;
-      if (m >= g.m) continue;
-      if constexpr (OUT == 1) {
-        uint16_t* yp = static_cast<uint16_t*>(g.y) + (int64_t)m * g.ld_y + n;
-        if (y_vec && n + 3 < g.n) {
-          *reinterpret_cast<uint2*>(yp) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (n + r < g.n) yp[r] = (uint16_t)(pack_bf16(y[r], 0.f) & 0xFFFFu);
-        }
-      } else {
-        float* yp = static_cast<float*>(g.y) + (int64_t)m * g.ld_y + n;
-        if (y_vec && n + 3 < g.n) {
-          *reinterpret_cast<float4*>(yp) = make_float4(y[0], y[1], y[2], y[3]);
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (n + r < g.n) yp[r] = y[r];
-        }
-      }
+    finish<GLU>(f, e, v, u);
+    const int m = m0 + 16 * mg + lr;
+    if constexpr (OUT == 2) {
+      if (f.h32) hadamard_lanes(v[0], v[1], lane);
+      store_requant(g, m, n0, v[0], v[1], lane);
+    } else {
+      const int n = n0 + 16 * p + 4 * lg;
+      if (m < g.m) store4<OUT == 1>(g, m, n, v[0], y_vec);
     }
   }
 }
 
-template <int MG, int PG, int OUT, bool GLU>
-void launch(const FusedArgs& f, hipStream_t s) {
-  constexpr int NG = GLU ? 2 * PG : PG;
-  constexpr int NCH = NG * MG > 4 && NG == 4 ? CH / 2 : CH;   // 64 weight rows and several M groups: half the chunk
+// K steps per register chunk: 8, or 4 where a chunk of 8 weight and activation
+// fragments beside the accumulators spills (256 registers per lane).
+constexpr int chunk_steps(int mg, int ng, bool tiled) {
+  const int regs = CH * (5 * ng + (mg > 1 ? 10 : 5)) + 4 * ng * mg;
+  return tiled ? (mg == 1 || regs <= 180 ? CH : CH / 2) : (mg <= 2 && regs <= 130 ? CH : CH / 2);
+}
+
+// The K split over the waves: mxfp4_gemm's (a chunk of 8 steps per wave, 8
+// waves at most), but 4 waves, of 4 steps each, where that gives fewer: short K
+// leaves the chip with too few loads in flight (16 rows x 2048 -> 2 x 5632,
+// MXFP4 output: 6.5 instead of 6.8 us; 64 rows 9.3 instead of 13.2).  It
+// depends on K alone, so dense and MXFP4 outputs are made of the same sums.
+void fused_split(int k, int& nwaves, int& spw) {
+  wave_split(k, nwaves, spw);
+  if (nwaves >= 4) return;
+  const int nsteps = (k + 127) / 128;
+  nwaves = nsteps < 8 ? 1 : nsteps < 16 ? nsteps / 4 : 4;
+  spw = (nsteps + nwaves - 1) / nwaves;
+}
+
+template <int MG, int PG, int OUT, bool GLU, bool TILED>
+void launch_layout(const FusedArgs& f, hipStream_t s) {
+  constexpr int NCH = chunk_steps(MG, GLU ? 2 * PG : PG, TILED);
   int nwaves, spw;
-  wave_split(f.g.k, nwaves, spw);
+  fused_split(f.g.k, nwaves, spw);
   const size_t ybytes = f.g.y_bf16 ? 2 : 4;
   const int y_vec = (((uintptr_t)f.g.y) % (4 * ybytes) == 0) && (f.g.ld_y % 4 == 0);
   const dim3 grid((f.g.n + 16 * PG - 1) / (16 * PG), (f.g.m + 16 * MAXMG - 1) / (16 * MAXMG));
-  if (f.g.tiled)
-    gemm_fused_small_kernel<MG, PG, OUT, true, GLU, NCH><<<grid, 64 * nwaves, 0, s>>>(f, spw, y_vec);
+  if (NCH == CH && spw > CH / 2)
+    gemm_fused_small_kernel<MG, PG, OUT, TILED, GLU, NCH><<<grid, 64 * nwaves, 0, s>>>(f, spw, y_vec);
   else
-    gemm_fused_small_kernel<MG, PG, OUT, false, GLU, NCH><<<grid, 64 * nwaves, 0, s>>>(f, spw, y_vec);
+    gemm_fused_small_kernel<MG, PG, OUT, TILED, GLU, CH / 2><<<grid, 64 * nwaves, 0, s>>>(f, spw, y_vec);
 }
 
-// PG: output column groups of 16 per workgroup for dense outputs
+template <int MG, int PG, int OUT, bool GLU>
+void launch(const FusedArgs& f, hipStream_t s) {
+  if (f.g.tiled) launch_layout<MG, PG, OUT, GLU, true>(f, s);
+  else launch_layout<MG, PG, OUT, GLU, false>(f, s);
+}
+
+// PG: output column groups of 16 per workgroup for plain dense outputs
 template <int MG, int PG>
 void launch_mg(const FusedArgs& f, hipStream_t s) {
   if (f.glu) {
@@ -219,9 +398,13 @@ void launch_mg(const FusedArgs& f, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_fused_small(const FusedArgs& f, hipStream_t s) {
+  // Up to 32 rows, two column groups share each activation fragment, unless
+  // that leaves CUs without a workgroup (16 rows x 14336 -> 4096: 11.4 us with
+  // 128 workgroups, 9.5 with 256).
+  const bool wide = (f.g.n + 31) / 32 >= cu_count();
   switch (f.g.m > 16 * MAXMG ? MAXMG : (f.g.m + 15) / 16) {
-    case 1: launch_mg<1, 2>(f, s); break;
-    case 2: launch_mg<2, 2>(f, s); break;
+    case 1: wide ? launch_mg<1, 2>(f, s) : launch_mg<1, 1>(f, s); break;
+    case 2: wide ? launch_mg<2, 2>(f, s) : launch_mg<2, 1>(f, s); break;
     case 3: launch_mg<3, 1>(f, s); break;
     default: launch_mg<4, 1>(f, s); break;
   }

@@ -79,6 +79,22 @@ __device__ __forceinline__ void store4(const GemmArgs& g, int m, int n, const v4
   }
 }
 
+// Tiled operands: the scale bytes of one K step of a 16-row fragment are 64
+// contiguous bytes (row-major [16][4]).  Lane (r, g) loads the dword of row r
+// for step s0 + 4 i + g, i.e. the scales of all four blocks of that step; the
+// scale of step s0 + 4 i + j for the lane's own block g then sits in byte g of
+// lane (r, j)'s dword.  One dword load replaces four byte loads.
+template <int NCH>
+__device__ __forceinline__ void scales_dw(const Operand& o, int s0, int lane, int (&sc)[NCH]) {
+  const int lr = lane & 15, lg = lane >> 4;
+#pragma unroll
+  for (int i = 0; i < NCH / 4; ++i) {
+    const int dw = *reinterpret_cast<const int*>(o.scale_row + (int64_t)(s0 + 4 * i + lg) * o.sstride);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sc[4 * i + j] = __shfl(dw, 16 * j + lr) >> (8 * lg);
+  }
+}
+
 // OUT: 0 fp32 Y, 1 bf16 Y, 2 MXFP4 Y (NG == 2: one 32-block of each output
 // row per workgroup).
 template <int MG, int NG, int OUT, bool TILED>
@@ -112,7 +128,68 @@ __global__ __launch_bounds__(64 * MAXW) void gemm_small_kernel(GemmArgs g, int s
 #pragma unroll
     for (int mg = 0; mg < MG; ++mg) acc[q][mg] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  k_loop<MG, NG, TILED, CH>(w, x, acc, s_begin, s_end, kblocks, lane);
+  for (int s0 = s_begin; s0 < s_end; s0 += CH) {
+    // every step of the chunk inside this wave's range and inside K
+    const bool full = s0 + CH <= s_end && (TILED || 4 * (s0 + CH) <= kblocks);
+    u32x4 wf[NG][CH];
+    int ws[NG][CH];
+    if (full) {
+#pragma unroll
+      for (int j = 0; j < CH; ++j)
+#pragma unroll
+        for (int q = 0; q < NG; ++q) {
+          wf[q][j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w[q].code + (s0 + j) * w[q].cstride));
+          if constexpr (!TILED) ws[q][j] = w[q].scale[(s0 + j) * w[q].sstride];
+        }
+      if constexpr (TILED) {
+#pragma unroll
+        for (int q = 0; q < NG; ++q) scales_dw<CH>(w[q], s0, lane, ws[q]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < CH; ++j)
+#pragma unroll
+        for (int q = 0; q < NG; ++q) {
+          const int s = s0 + j;
+          wf[q][j] = u32x4{0u, 0u, 0u, 0u};
+          ws[q][j] = 0;
+          if (s < s_end && (TILED || 4 * s + lg < kblocks)) {
+            wf[q][j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w[q].code + s * w[q].cstride));
+            ws[q][j] = w[q].scale[s * w[q].sstride];
+          }
+        }
+    }
+#pragma unroll
+    for (int mg = 0; mg < MG; ++mg) {
+      u32x4 xf[CH];
+      int xs[CH];
+      if (full) {
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+          xf[j] = *reinterpret_cast<const u32x4*>(x[mg].code + (s0 + j) * x[mg].cstride);
+          if constexpr (!TILED) xs[j] = x[mg].scale[(s0 + j) * x[mg].sstride];
+        }
+        if constexpr (TILED) scales_dw<CH>(x[mg], s0, lane, xs);
+      } else {
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+          const int s = s0 + j;
+          xf[j] = u32x4{0u, 0u, 0u, 0u};
+          xs[j] = 0;
+          if (s < s_end && (TILED || 4 * s + lg < kblocks)) {
+            xf[j] = *reinterpret_cast<const u32x4*>(x[mg].code + s * x[mg].cstride);
+            xs[j] = x[mg].scale[s * x[mg].sstride];
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < CH; ++j)
+        if (s0 + j < s_end) {
+#pragma unroll
+          for (int q = 0; q < NG; ++q) acc[q][mg] = mma(wf[q][j], xf[j], acc[q][mg], ws[q][j], xs[j]);
+        }
+    }
+  }
 
   // lane holds Y[m0 + 16 mg + lr][n .. n + 3] of weight group q
   auto store_frag = [&](int q, int mg, const v4f& v) {

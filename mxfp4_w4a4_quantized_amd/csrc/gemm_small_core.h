@@ -1,6 +1,6 @@
 // Shared parts of the small-M kernels (gemm_small.hip, gemm_fused_small.hip):
-// operand addressing and loads, the K loop over one wave's range of steps, and
-// the K split.  The design is described in gemm_small.hip.
+// operand addressing, the MXFP4 store and the K split.  The design is described
+// in gemm_small.hip.
 #pragma once
 #include "internal.h"
 #include "block_quant.h"
@@ -67,22 +67,6 @@ __device__ __forceinline__ Operand operand(const uint8_t* codes, const uint8_t* 
   return o;
 }
 
-// Tiled operands: the scale bytes of one K step of a 16-row fragment are 64
-// contiguous bytes (row-major [16][4]).  Lane (r, g) loads the dword of row r
-// for step s0 + 4 i + g, i.e. the scales of all four blocks of that step; the
-// scale of step s0 + 4 i + j for the lane's own block g then sits in byte g of
-// lane (r, j)'s dword.  One dword load replaces four byte loads.
-template <int NCH>
-__device__ __forceinline__ void scales_dw(const Operand& o, int s0, int lane, int (&sc)[NCH]) {
-  const int lr = lane & 15, lg = lane >> 4;
-#pragma unroll
-  for (int i = 0; i < NCH / 4; ++i) {
-    const int dw = *reinterpret_cast<const int*>(o.scale_row + (int64_t)(s0 + 4 * i + lg) * o.sstride);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) sc[4 * i + j] = __shfl(dw, 16 * j + lr) >> (8 * lg);
-  }
-}
-
 // MXFP4 output of the small-M kernel: Y requantized per 32-block along N by
 // the quantizer's rule, from the same fp32 sums that the fp32 output stores.
 // The workgroup's 32 weight rows (NG = 2) are one block of each output row:
@@ -124,78 +108,6 @@ __device__ __forceinline__ void store_requant(const GemmArgs& g, int m, int n0, 
   } else {
     *reinterpret_cast<uint4*>(g.q_codes + (int64_t)m * (g.n >> 1) + 16 * blk) = codes;
     g.q_scales[(int64_t)m * (g.n >> 5) + blk] = (uint8_t)sbyte;
-  }
-}
-
-// One wave's K range [s_begin, s_end) into its accumulator tiles: NG weight
-// fragments against MG activation fragments per step, the steps in ascending
-// order whatever the chunk length NCH, so that every kernel that takes the
-// same split forms the same sums.
-template <int MG, int NG, bool TILED, int NCH>
-__device__ __forceinline__ void k_loop(const Operand (&w)[NG], const Operand (&x)[MG], v4f (&acc)[NG][MG], int s_begin,
-                                       int s_end, int kblocks, int lane) {
-  const int lg = lane >> 4;
-  for (int s0 = s_begin; s0 < s_end; s0 += NCH) {
-    // every step of the chunk inside this wave's range and inside K
-    const bool full = s0 + NCH <= s_end && (TILED || 4 * (s0 + NCH) <= kblocks);
-    u32x4 wf[NG][NCH];
-    int ws[NG][NCH];
-    if (full) {
-#pragma unroll
-      for (int j = 0; j < NCH; ++j)
-#pragma unroll
-        for (int q = 0; q < NG; ++q) {
-          wf[q][j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w[q].code + (s0 + j) * w[q].cstride));
-          if constexpr (!TILED) ws[q][j] = w[q].scale[(s0 + j) * w[q].sstride];
-        }
-      if constexpr (TILED) {
-#pragma unroll
-        for (int q = 0; q < NG; ++q) scales_dw<NCH>(w[q], s0, lane, ws[q]);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < NCH; ++j)
-#pragma unroll
-        for (int q = 0; q < NG; ++q) {
-          const int s = s0 + j;
-          wf[q][j] = u32x4{0u, 0u, 0u, 0u};
-          ws[q][j] = 0;
-          if (s < s_end && (TILED || 4 * s + lg < kblocks)) {
-            wf[q][j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w[q].code + s * w[q].cstride));
-            ws[q][j] = w[q].scale[s * w[q].sstride];
-          }
-        }
-    }
-#pragma unroll
-    for (int mg = 0; mg < MG; ++mg) {
-      u32x4 xf[NCH];
-      int xs[NCH];
-      if (full) {
-#pragma unroll
-        for (int j = 0; j < NCH; ++j) {
-          xf[j] = *reinterpret_cast<const u32x4*>(x[mg].code + (s0 + j) * x[mg].cstride);
-          if constexpr (!TILED) xs[j] = x[mg].scale[(s0 + j) * x[mg].sstride];
-        }
-        if constexpr (TILED) scales_dw<NCH>(x[mg], s0, lane, xs);
-      } else {
-#pragma unroll
-        for (int j = 0; j < NCH; ++j) {
-          const int s = s0 + j;
-          xf[j] = u32x4{0u, 0u, 0u, 0u};
-          xs[j] = 0;
-          if (s < s_end && (TILED || 4 * s + lg < kblocks)) {
-            xf[j] = *reinterpret_cast<const u32x4*>(x[mg].code + s * x[mg].cstride);
-            xs[j] = x[mg].scale[s * x[mg].sstride];
-          }
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < NCH; ++j)
-        if (s0 + j < s_end) {
-#pragma unroll
-          for (int q = 0; q < NG; ++q) acc[q][mg] = mma(wf[q][j], xf[j], acc[q][mg], ws[q][j], xs[j]);
-        }
-    }
   }
 }
 
