@@ -22,14 +22,19 @@ constexpr int NONE = 0, RELU = 1, SILU = 2, GELU = 3, GELU_TANH = 4;   // mxfp4_
 
 __device__ __forceinline__ float relu(float x) { return x < 0.0f ? 0.0f : x; }   // keeps NaN
 
-__device__ __forceinline__ float silu(float x) {
-  return x * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.442695040889f));
+// x / (1 + 2^t) with both sides of the quotient scaled by 2^-24 (one multiply
+// more): v_rcp_f32 flushes results below 2^-126, which 1 / (1 + 2^t) reaches
+// while x times it is still a normal number.
+__device__ __forceinline__ float over_one_plus_exp2(float x, float t) {
+  constexpr float c = 1.0f / 16777216.0f;
+  return (x * c) * __builtin_amdgcn_rcpf(__builtin_fmaf(__builtin_amdgcn_exp2f(t), c, c));
 }
+
+__device__ __forceinline__ float silu(float x) { return over_one_plus_exp2(x, x * -1.442695040889f); }
 
 __device__ __forceinline__ float gelu_tanh(float x) {
   // -log2(e) * 2 sqrt(2/pi) and that times 0.044715
-  const float t = x * __builtin_fmaf(-0.10294324f, x * x, -2.3022082f);
-  return x * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t));
+  return over_one_plus_exp2(x, x * __builtin_fmaf(-0.10294324f, x * x, -2.3022082f));
 }
 
 __device__ __forceinline__ float gelu(float x) {

@@ -134,7 +134,8 @@ mxfp4_status launch_fused(const mxfp4::FusedArgs& f, void* stream) {
   const hipStream_t s = static_cast<hipStream_t>(stream);
   switch (mxfp4::fused_route(f)) {
     case mxfp4::FusedRoute::kSmall: return from_hip(mxfp4::launch_fused_small(f, s));
-    case mxfp4::FusedRoute::kLarge: return from_hip(mxfp4::launch_fused_large(f, s));
+    case mxfp4::FusedRoute::kMid: return from_hip(mxfp4::launch_fused_tiles(f, true, s));
+    case mxfp4::FusedRoute::kLarge: return from_hip(mxfp4::launch_fused_tiles(f, false, s));
     default: return MXFP4_ERR_UNSUPPORTED;
   }
 }

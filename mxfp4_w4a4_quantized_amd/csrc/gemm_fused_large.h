@@ -34,13 +34,36 @@
 namespace mxfp4 {
 namespace large {
 
-constexpr int WN = 2, WM = 2, NW = WN * WM, NT = 64 * NW;
-constexpr int FN = BN / WN / 32, FM = BM / WM / 32;
-constexpr int CODE_LOADS = CODE_BYTES / 1024 / NW;   // per wave and stage, 16 B per lane
-constexpr int SCALE_LOADS = ROWS * 4 / 256 / NW;     // per wave and stage, 4 B per lane
-constexpr int LPS = CODE_LOADS + SCALE_LOADS;
-constexpr int CODE_LOADS_B = CODE_LOADS / 2;         // issued during sub-step 0
-constexpr int NRD = FN + FM;                         // fragment reads per sub-step
+// A workgroup's output tile: TBN weight rows x TBM activation rows on 2 x 2
+// waves, a ring of TNBUF stages, TWGS workgroups per CU.
+template <int TBN, int TBM, int TNBUF, int TWGS>
+struct Tile {
+  static constexpr int BN = TBN, BM = TBM, NBUF = TNBUF, WGS = TWGS;
+  static constexpr int WN = 2, WM = 2, NW = WN * WM, NT = 64 * NW;
+  static constexpr int ROWS = BN + BM;                        // rows per stage: W then X
+  static constexpr int CODE_BYTES = ROWS * RB;
+  static constexpr int STAGE_BYTES = CODE_BYTES + ROWS * 4;
+  static constexpr int FN = BN / WN / 32, FM = BM / WM / 32;  // 32 x 32 fragments per wave
+  // Per stage and wave: code loads of 1 KiB (16 rows), in stage row order, and
+  // scale loads of 64 rows (the last one repeated where they do not divide).
+  static constexpr int CODE_LOADS = ROWS / 16 / NW, SCALE_LOADS = (ROWS / 64 + NW - 1) / NW;
+  static constexpr int LPS = CODE_LOADS + SCALE_LOADS;
+  static constexpr int CODE_LOADS_B = CODE_LOADS / 2;         // issued during sub-step 0
+  static constexpr int NRD = FN + FM;                         // fragment reads per sub-step
+  static constexpr bool WHOLE = BN % (16 * CODE_LOADS) == 0;  // no wave loads rows of both sides
+  static_assert(ROWS % (16 * NW) == 0 && BN % 64 == 0, "whole loads per wave and side");
+  static_assert(TWGS * TNBUF * STAGE_BYTES <= 160 * 1024, "LDS ring exceeds 160 KiB");
+};
+
+// Direct global -> LDS loads of 16 and 4 bytes per lane.  (Functions of their
+// own: inside a template that depends on the tile, the host pass drops the
+// kernel's launch stub over the builtins.)
+__device__ __forceinline__ void load_lds16(const uint8_t* src, uint8_t* dst) {
+  __builtin_amdgcn_global_load_lds(src, dst, 16, 0, 0);
+}
+__device__ __forceinline__ void load_lds4(const uint8_t* src, uint8_t* dst) {
+  __builtin_amdgcn_global_load_lds(src, dst, 4, 0, 0);
+}
 
 // Activation classes of the kernels that apply it in registers.
 constexpr int A_LINEAR = 0;   // none or relu, by f.act
@@ -122,14 +145,19 @@ __device__ __forceinline__ void hadamard_fragment(float (&v)[16]) {
 }
 
 // ACT: A_LINEAR or an mxfp4_act.  OUT: 0 fp32, 1 bf16, 2 MXFP4.  RES: 0 no gate
-// or residual, 1 / 2 a gate and/or a residual, the residual bf16 / fp32.
-template <int ACT, int OUT, int RES, bool GLU>
-__global__ __launch_bounds__(NT, 1) void gemm_fused_large_kernel(FusedArgs f, int tiles_m, int tiles_n, int grid,
+// or residual; 1 / 2 a gate and/or a residual (bf16 / fp32) in whole aligned
+// pieces of 4 columns, with at most two gate rows per wave; 3 any other.
+template <class T, int ACT, int OUT, int RES, bool GLU>
+__global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(FusedArgs f, int tiles_m, int tiles_n, int grid,
                                                                  int xcd_remap) {
   static_assert(RES == 0 || (OUT != 2 && !GLU), "gate and residual are for plain dense outputs");
+  constexpr int BN = T::BN, BM = T::BM, NBUF = T::NBUF, WN = T::WN, WM = T::WM, NW = T::NW, FN = T::FN, FM = T::FM;
+  constexpr int CODE_BYTES = T::CODE_BYTES, STAGE_BYTES = T::STAGE_BYTES, LPS = T::LPS, NRD = T::NRD;
+  constexpr int CODE_LOADS = T::CODE_LOADS, SCALE_LOADS = T::SCALE_LOADS, CODE_LOADS_B = T::CODE_LOADS_B;
   constexpr int TN = GLU ? BN / 2 : BN;          // output columns per tile
   constexpr int WCOLS = TN / WN;                 // and per wave
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[NBUF * STAGE_BYTES];
+  constexpr bool PIECES = RES == 1 || RES == 2;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[NBUF * STAGE_BYTES + (PIECES && FM * FN == 4 ? 1024 : 0)];
 
   const GemmArgs& g = f.g;
   const int ntiles = tiles_m * tiles_n;
@@ -143,40 +171,64 @@ __global__ __launch_bounds__(NT, 1) void gemm_fused_large_kernel(FusedArgs f, in
   const uint32_t kbytes = (uint32_t)g.k / 2, kblocks = (uint32_t)g.k / 32;
   const int lr = lane & 31, lg = lane >> 5;
 
-  // ---- direct LDS load plan, as gemm_large_kernel's.  Gated: 32-row group q
-  // of the weight side holds rows of G (q even) or U (q odd); a code load
+  // ---- direct LDS load plan, as gemm_large_kernel's: load i of a wave fills 16
+  // stage rows (codes) or 64 (scales), weight rows first.  Gated: 32-row group
+  // q of the weight side holds rows of G (q even) or U (q odd); a code load
   // takes 16 rows of one group, a scale load 64 rows (lanes 0-31 G, 32-63 U).
-  const bool w_side = wave < NW / 2;
-  const uint8_t* cbase[2] = {w_side ? g.b_codes : g.a_codes, GLU && w_side ? f.u_codes : w_side ? g.b_codes : g.a_codes};
-  const uint8_t* sbase = !w_side ? g.a_scales : GLU && lane >= 32 ? f.u_scales : g.b_scales;
-  const int lim = (w_side ? g.n : g.m) - 1;
-  const int part = wave % (NW / 2);
-  uint32_t coff[CODE_LOADS], soff[SCALE_LOADS];
   const bool tiled = g.tiled;
   const uint32_t nstage = (uint32_t)nk;
+  const bool w_first = CODE_LOADS * wave < BN / 16;   // this wave's first load: weight side
+  auto code_group = [&](int i) { return CODE_LOADS * wave + i; };              // 16-row group of the stage
+  auto code_w = [&](int i) { return T::WHOLE ? w_first : code_group(i) < BN / 16; };
+  auto scale_group = [&](int i) { return min(SCALE_LOADS * wave + i, T::ROWS / 64 - 1); };
+  auto scale_w = [&](int i) { return T::WHOLE ? w_first : scale_group(i) < BN / 64; };
+  // The operands' addresses in registers, and selects between values (the
+  // unary +): left to itself the compiler selects between the addresses of the
+  // arguments, which puts a copy of them into scratch memory.
+  auto held = [](const uint8_t* p) {
+    uint64_t v = (uint64_t)p;
+    asm("" : "+s"(v));
+    return v;
+  };
+  const uint64_t pa = held(g.a_codes), pb = held(g.b_codes), pu = GLU ? held(f.u_codes) : pb;
+  const uint64_t qa = held(g.a_scales), qb = held(g.b_scales), qu = GLU ? held(f.u_scales) : qb;
+  // Base of a wave's code loads: one, or two in turn where its loads alternate
+  // between G and U; a base for each load where a wave serves both sides.
+  constexpr int NCB = !T::WHOLE ? CODE_LOADS : GLU ? 2 : 1;
+  auto cb = [](int i) { return NCB == CODE_LOADS ? i : NCB == 2 ? (i >> 1) & 1 : 0; };
+  const uint8_t *cbase[NCB], *sbase[SCALE_LOADS];
+#pragma unroll
+  for (int i = 0; i < NCB; ++i) {
+    const int q = NCB == 2 ? 2 * i : code_group(i);   // (a wave's load count is a multiple of 4)
+    cbase[i] = reinterpret_cast<const uint8_t*>(!code_w(i) ? +pa : (q & 2) ? +pu : +pb);
+  }
+#pragma unroll
+  for (int i = 0; i < SCALE_LOADS; ++i)
+    sbase[i] = reinterpret_cast<const uint8_t*>(!scale_w(i) ? +qa : lane >= 32 ? +qu : +qb);
+  uint32_t coff[CODE_LOADS], soff[SCALE_LOADS];
   auto plan = [&](int j) {   // j-th tile of this workgroup
     int tm, tn;
     tile_coords(j * grid + slot, tiles_m, tiles_n, tm, tn);
-    // first row, and the row of 16-row group rgp / of scale row r within it
-    const int r0 = w_side ? tn * TN : tm * BM;
-    auto group_row = [&](int rgp) { return GLU && w_side ? 32 * (rgp >> 2) + 16 * (rgp & 1) : 16 * rgp; };
 #pragma unroll
     for (int i = 0; i < CODE_LOADS; ++i) {
-      const int row0 = r0 + group_row(CODE_LOADS * part + i);
+      const int q = code_group(i);
+      const bool w = code_w(i);
+      const int row0 = w ? tn * TN + (GLU ? 32 * (q >> 2) + 16 * (q & 1) : 16 * q) : tm * BM + 16 * q - BN;
       if (tiled) {
         coff[i] = (uint32_t)(row0 >> 8) * nstage * (16 * 1024) + (uint32_t)(row0 & 255) * 64 + lane * 16;
       } else {
         const int row = row0 + (lane >> 2);
-        const uint32_t grow = (uint32_t)min(row, lim);
+        const uint32_t grow = (uint32_t)min(row, (w ? g.n : g.m) - 1);
         coff[i] = grow * kbytes + 16u * (uint32_t)((lane & 3) ^ swz(row & 255));
       }
     }
 #pragma unroll
     for (int i = 0; i < SCALE_LOADS; ++i) {
-      const int sr = 64 * (SCALE_LOADS * part + i);
-      const int row = r0 + (GLU && w_side ? sr / 2 + lr : sr + lane);
+      const int q = scale_group(i);
+      const bool w = scale_w(i);
+      const int row = w ? tn * TN + (GLU ? 32 * q + lr : 64 * q + lane) : tm * BM + 64 * q - BN + lane;
       soff[i] = tiled ? (uint32_t)(row >> 8) * nstage * 1024 + (uint32_t)(row & 255) * 4
-                      : (uint32_t)min(row, lim) * kblocks;
+                      : (uint32_t)min(row, (w ? g.n : g.m) - 1) * kblocks;
     }
   };
   const uint32_t cstride = tiled ? 16 * 1024 : RB, sstride = tiled ? 1024 : 4;   // bytes per stage
@@ -186,15 +238,13 @@ __global__ __launch_bounds__(NT, 1) void gemm_fused_large_kernel(FusedArgs f, in
     uint8_t* dst = lds + ibuf * STAGE_BYTES;
 #pragma unroll
     for (int i = i0; i < i1; ++i)
-      __builtin_amdgcn_global_load_lds(cbase[GLU ? (i >> 1) & 1 : 0] + ikt * cstride + coff[i],
-                                       dst + (CODE_LOADS * wave + i) * 1024, 16, 0, 0);
+      load_lds16(cbase[cb(i)] + ikt * cstride + coff[i], dst + code_group(i) * 1024);
   };
   auto issue_scales = [&]() {
-    uint8_t* dst = lds + ibuf * STAGE_BYTES;
+    uint8_t* dst = lds + ibuf * STAGE_BYTES + CODE_BYTES;
 #pragma unroll
     for (int i = 0; i < SCALE_LOADS; ++i)
-      __builtin_amdgcn_global_load_lds(sbase + ikt * sstride + soff[i],
-                                       dst + CODE_BYTES + (64 * (SCALE_LOADS * wave + i)) * 4, 4, 0, 0);
+      load_lds4(sbase[i] + ikt * sstride + soff[i], dst + 256 * scale_group(i));
   };
   auto advance = [&]() {
     ibuf = ibuf + 1 == NBUF ? 0 : ibuf + 1;
@@ -266,13 +316,39 @@ __global__ __launch_bounds__(NT, 1) void gemm_fused_large_kernel(FusedArgs f, in
   load_scales(lds, sw, sx);
   load_frags(lds, 0, wa, xa);
 
+  // 128 x 128 tiles: the residual of a tile is asked for PF stages before its
+  // epilogue, one 4-byte load (into LDS that nobody reads) for every 128-byte
+  // line of the wave's block, so that the epilogue's loads hit in L2 (2048 x
+  // 14336 -> 4096: 74.7 -> 70.6 us).  The larger tiles lose more to the ring
+  // loads waiting behind these than they gain (16384 x 3072 -> 12288: 409
+  // against 425 us with it).
+  constexpr bool AHEAD = PIECES && FM * FN == 4;
+  constexpr int PF = 8;
+  auto prefetch_res = [&](int tm, int tn) {
+    constexpr int RSZ = RES == 1 ? 2 : 4, LINES = WCOLS * RSZ / 128;   // per row
+    const int mw0 = tm * BM + wm * (BM / WM), nw0 = tn * TN + wn * WCOLS;
+    const uint8_t* res = static_cast<const uint8_t*>(f.residual);
+#pragma unroll
+    for (int i = 0; i < BM / WM * LINES / 64; ++i) {
+      const int line = 64 * i + lane;
+      const int m = min(mw0 + line / LINES, g.m - 1), n = min(nw0 + line % LINES * (128 / RSZ), g.n - 4);
+      load_lds4(res + ((int64_t)m * f.ld_res + n) * RSZ, lds + NBUF * STAGE_BYTES + 256 * wave);
+    }
+  };
+
   int cbuf = 0;   // ring slot of the stage being computed
   for (int j = 0; j * nk < total; ++j) {
+    int tm, tn;
+    tile_coords(j * grid + slot, tiles_m, tiles_n, tm, tn);
+    const int ahead = AHEAD && f.residual != nullptr ? max(nk - PF, 0) : nk;
     // the compiler does not see the accumulators' start values being written
     // (inline asm): wait states before the K loop's MFMAs read them
     asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
 
     for (int kt = 0; kt < nk; ++kt) {
+      if constexpr (AHEAD) {
+        if (kt == ahead) prefetch_res(tm, tn);
+      }
       advance();   // to stage it + NBUF - 1
       wait_stages<NBUF - 3, LPS>();
       __builtin_amdgcn_s_barrier();
@@ -309,8 +385,6 @@ __global__ __launch_bounds__(NT, 1) void gemm_fused_large_kernel(FusedArgs f, in
     }
 
     // ---- epilogue of this workgroup's j-th tile
-    int tm, tn;
-    tile_coords(j * grid + slot, tiles_m, tiles_n, tm, tn);
     const int mw0 = tm * BM + wm * (BM / WM), nw0 = tn * TN + wn * WCOLS;   // the wave's block of Y
     if ((j + 1) * nk < total) load_bias(j + 1);   // the next tile's start values
     const bool relu = f.act == act::RELU;
@@ -395,63 +469,90 @@ __global__ __launch_bounds__(NT, 1) void gemm_fused_large_kernel(FusedArgs f, in
     } else {
       // Dense output, staged per wave in the ring slot of the stage just
       // computed (free until the next issue, which follows the next barrier):
-      // 32 rows of SB bytes per pass, padded to PITCH.  SE: bytes of a staged
+      // 32 rows of SB bytes per pass, 16-byte chunk c of row r at chunk
+      // c ^ (r % chunks), which spreads both the writes (32 rows, one chunk)
+      // and the reads (whole rows) over the banks.  SE: bytes of a staged
       // element (bf16 only where nothing is added after it).
       constexpr int SE = OUT == 1 && RES == 0 ? 2 : 4;
-      constexpr int FPP = SE == 2 ? NO : 2;                 // fragments per pass
-      constexpr int SB = FPP * 32 * SE, PITCH = SB + 16;
-      constexpr int LPR = SB / 16, RPI = 64 / LPR;          // lanes per row, rows per instruction
+      // fragments per pass: whole 256-byte rows where the ring slot holds them
+      constexpr int MAXF = (STAGE_BYTES / (NW * 32) >= 256 ? 256 : 128) / (32 * SE);
+      constexpr int FPP = NO < MAXF ? NO : MAXF;
+      constexpr int SB = FPP * 32 * SE;
+      constexpr int LPR = SB / 16, RPI = 64 / LPR;          // lanes (chunks) per row, rows per instruction
       constexpr int EPL = 16 / SE;                          // elements per lane
       constexpr int OSZ = OUT == 1 ? 2 : 4;                 // bytes of an output element
-      static_assert(NW * 32 * PITCH <= STAGE_BYTES, "staging area");
-      const bool y_st = ((uintptr_t)g.y % 16) == 0 && ((g.ld_y * OSZ) % 16) == 0;
-      bool full = y_st && (tm + 1) * BM <= g.m && (tn + 1) * TN <= g.n;
-      constexpr int RSZ = RES == 1 ? 2 : 4;
-      if constexpr (RES != 0) {
-        if (f.residual != nullptr)
-          full = full && ((uintptr_t)f.residual % (4 * RSZ)) == 0 && (f.ld_res % 4) == 0;
-      }
+      static_assert(NW * 32 * SB <= STAGE_BYTES, "staging area");
       const int lslot = cbuf == 0 ? NBUF - 1 : cbuf - 1;
-      uint8_t* tb = lds + lslot * STAGE_BYTES + wave * (32 * PITCH);
+      uint8_t* tb = lds + lslot * STAGE_BYTES + wave * (32 * SB);
       const int prow = lane / LPR, pcol = (lane % LPR) * EPL;   // this lane's piece of a row group
+      constexpr int NQ = NO / FPP, NP = FM * NQ;                // passes along N, passes
 
-      // residual pieces of one pass (full tiles), loaded a pass ahead
+      // RES 1 and 2: residual and output through buffer instructions from the
+      // wave's first row on: rows past m are out of range (loads give 0, stores
+      // are dropped), and so are columns past n (an offset of 2^31), so edge
+      // tiles need no branches, which cost a wait for every load in flight
+      // where they join.  Residual pieces are loaded RD - 1 passes ahead: the
+      // bytes in flight bound its rate.
       typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
       typedef uint32_t rvec __attribute__((ext_vector_type(RES == 1 ? 2 : 4)));   // 4 elements
-      rvec rres[2][32 / RPI];
-      auto load_res = [&](int p, rvec (&dst)[32 / RPI]) {
-        const int m0 = mw0 + 32 * (p / (NO / FPP)), n0 = nw0 + (p % (NO / FPP)) * (FPP * 32) + pcol;
-#pragma unroll
-        for (int r = 0; r < 32 / RPI; ++r)
-          dst[r] = __builtin_nontemporal_load(reinterpret_cast<const rvec*>(
-              static_cast<const uint8_t*>(f.residual) + ((int64_t)(m0 + RPI * r + prow) * f.ld_res + n0) * RSZ));
+      constexpr int RSZ = RES == 1 ? 2 : 4;
+      constexpr int RD = FM * FN > 4 ? 2 : NP < 4 ? NP : 4;
+      constexpr int kNonTemporal = 2;   // buffer cache policy nt
+      rvec rres[RD][32 / RPI];
+      const int rows = max(0, min(BM / WM, g.m - mw0));
+      const int64_t first = PIECES && rows > 0 ? mw0 : 0;
+      uint32_t ldr = (uint32_t)f.ld_res * RSZ, ldy = (uint32_t)g.ld_y * OSZ;   // row strides, bytes
+      // (opaque here: else every row's offset is held in a register over all tiles)
+      asm volatile("" : "+s"(ldr), "+s"(ldy));
+      const __amdgpu_buffer_rsrc_t rr = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<uint8_t*>(static_cast<const uint8_t*>(f.residual)) + first * f.ld_res * RSZ, 0, rows * ldr, 0x00020000);
+      const __amdgpu_buffer_rsrc_t yr =
+          __builtin_amdgcn_make_buffer_rsrc(static_cast<uint8_t*>(g.y) + first * g.ld_y * OSZ, 0, rows * ldy, 0x00020000);
+      auto column = [&](int q) { return nw0 + q * (FPP * 32) + pcol; };
+      auto offset = [&](int p, int r, uint32_t ld, int size) {
+        const int n = column(p % NQ);
+        return (n < g.n ? (uint32_t)n * size : 0x80000000u) + (uint32_t)(32 * (p / NQ) + RPI * r + prow) * ld;
       };
-      constexpr int NP = FM * (NO / FPP);
-      const bool res_ahead = RES != 0 && full && f.residual != nullptr;
-      // one gate row for the wave's whole block of rows (full tiles): its values
-      // for this lane's columns of each pass along N
-      f32x4 grow[NO / FPP];
-      bool one_group = true;
-      if constexpr (RES != 0) {
-        if (res_ahead) load_res(0, rres[0]);
-        if (f.gate != nullptr) {
-          const uint32_t g0 = (uint32_t)mw0 / f.group_rows;
-          one_group = (uint32_t)min(mw0 + BM / WM, g.m) <= (g0 + 1) * (uint64_t)f.group_rows;
-          if (one_group && full) {
+      auto load_res = [&](int p) {
 #pragma unroll
-            for (int q = 0; q < NO / FPP; ++q)
+        for (int r = 0; r < 32 / RPI; ++r) {
+          const int at = (int)offset(p, r, ldr, RSZ);
+          if constexpr (RES == 1) rres[p % RD][r] = __builtin_amdgcn_raw_buffer_load_b64(rr, at, 0, kNonTemporal);
+          else rres[p % RD][r] = __builtin_amdgcn_raw_buffer_load_b128(rr, at, 0, kNonTemporal);
+        }
+      };
+      // Gate values of this lane's columns: a wave's rows lie in two groups at
+      // most, the rows from `next` on in the second.
+      f32x4 gate[2][NQ];
+      int next = 0;
+      if constexpr (PIECES) {
+        if (f.residual != nullptr) {
+#pragma unroll
+          for (int p = 0; p < RD - 1 && p < NP; ++p) load_res(p);
+        }
+        if (f.gate != nullptr) {
+          const uint32_t g0 = (uint32_t)min(mw0, g.m - 1) / f.group_rows, groups = (uint32_t)(g.m - 1) / f.group_rows;
+          next = (int)min((g0 + 1) * (uint64_t)f.group_rows, (uint64_t)g.m);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int q = 0; q < NQ; ++q)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                grow[q][e] = vec_elem(f.gate, f.vec_bf16, (int64_t)g0 * f.ld_gate + nw0 + q * (FPP * 32) + pcol + e);
-          }
+                gate[i][q][e] = vec_elem(f.gate, f.vec_bf16, (int64_t)min(g0 + i, groups) * f.ld_gate +
+                                                                 min(column(q) + e, g.n - 1));
         }
       }
+      // RES 0: whole aligned pieces, and nothing to leave out of the tile
+      const bool vec = ((uintptr_t)g.y % 16) == 0 && ((g.ld_y * OSZ) % 16) == 0;
+      const bool full = vec && (tm + 1) * BM <= g.m && (tn + 1) * TN <= g.n;
       __builtin_amdgcn_s_barrier();   // every wave is done reading that slot
       each([&](auto pass) __attribute__((always_inline)) {
         constexpr int p = pass;
-        constexpr int bb = p / (NO / FPP), q = p % (NO / FPP), o0 = q * FPP;
-        if constexpr (RES != 0) {
-          if (res_ahead && p + 1 < NP) load_res(p + 1, rres[(p + 1) & 1]);
+        constexpr int bb = p / NQ, q = p % NQ, o0 = q * FPP;
+        const int m0 = mw0 + 32 * bb + prow, n0 = column(q);
+        if constexpr (PIECES) {
+          if (f.residual != nullptr && p + RD - 1 < NP) load_res(p + RD - 1);
         }
 #pragma unroll
         for (int o = o0; o < o0 + FPP; ++o) {
@@ -459,7 +560,8 @@ __global__ __launch_bounds__(NT, 1) void gemm_fused_large_kernel(FusedArgs f, in
           take(o, bb, v);
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            uint8_t* dst = tb + lr * PITCH + ((o - o0) * 32 + 8 * t + 4 * lg) * SE;
+            const int at = ((o - o0) * 32 + 8 * t + 4 * lg) * SE;
+            uint8_t* dst = tb + lr * SB + (((at >> 4) ^ (lr & (LPR - 1))) << 4) + (at & 15);
             if constexpr (SE == 2) {
               *reinterpret_cast<uint2*>(dst) =
                   make_uint2(pack_bf16(v[4 * t], v[4 * t + 1]), pack_bf16(v[4 * t + 2], v[4 * t + 3]));
@@ -469,83 +571,91 @@ __global__ __launch_bounds__(NT, 1) void gemm_fused_large_kernel(FusedArgs f, in
           }
         }
         // the area is private to this wave: its LDS writes land before its reads
-        const int m0 = mw0 + 32 * bb, n0 = nw0 + 32 * o0 + pcol;
         auto staged = [&](int r) {
-          return *reinterpret_cast<const u32x4*>(tb + (RPI * r + prow) * PITCH + (lane % LPR) * 16);
+          const int row = RPI * r + prow;
+          return *reinterpret_cast<const u32x4*>(tb + row * SB + (((lane % LPR) ^ (row & (LPR - 1))) << 4));
         };
-        auto out = [&](int m) { return static_cast<uint8_t*>(g.y) + ((int64_t)m * g.ld_y + n0) * OSZ; };
-        // gate of row m where the wave's rows span several groups
-        auto gate_rows = [&](int m, f32x4& x) {
-          const int64_t at = (int64_t)((uint32_t)m / f.group_rows) * f.ld_gate + n0;
+        if constexpr (RES == 0) {
+          uint8_t* const y0 = static_cast<uint8_t*>(g.y) + ((int64_t)m0 * g.ld_y + n0) * OSZ;
+          if (full) {
+            // non-temporal: Y streams out without displacing the operand panels
+            // the XCD's other workgroups still read from L2
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (n0 + e < g.n) x[e] *= vec_elem(f.gate, f.vec_bf16, at + e);
-        };
-        if (full) {
-#pragma unroll
-          for (int r = 0; r < 32 / RPI; ++r) {
-            const int m = m0 + RPI * r + prow;
-            const u32x4 s = staged(r);
-            // non-temporal stores: Y streams out without displacing the operand
-            // panels the XCD's other workgroups still read from L2
-            if constexpr (RES == 0) {
-              __builtin_nontemporal_store(s, reinterpret_cast<u32x4*>(out(m)));
-            } else {
-              f32x4 x = __builtin_bit_cast(f32x4, s);
-              if (f.gate != nullptr) {
-                if (one_group) x *= grow[q];
-                else gate_rows(m, x);
-              }
-              if (f.residual != nullptr) {
-                const rvec rv = rres[p & 1][r];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  if constexpr (RES == 1)
-                    x[e] += __uint_as_float(e & 1 ? rv[e >> 1] & 0xFFFF0000u : rv[e >> 1] << 16);
-                  else
-                    x[e] += __uint_as_float(rv[e]);
-                }
-              }
-              if constexpr (OUT == 1)
-                __builtin_nontemporal_store(u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])},
-                                            reinterpret_cast<u32x2*>(out(m)));
-              else
-                __builtin_nontemporal_store(x, reinterpret_cast<f32x4*>(out(m)));
-            }
-          }
-        } else {
-          // edge tiles and unaligned rows: bounds-checked, element by element
-          // where a 16-byte piece does not fit (a rolled loop: little code)
+            for (int r = 0; r < 32 / RPI; ++r)
+              __builtin_nontemporal_store(staged(r), reinterpret_cast<u32x4*>(y0 + (int64_t)r * RPI * g.ld_y * OSZ));
+          } else {
 #pragma unroll 1
-          for (int r = 0; r < 32 / RPI; ++r) {
-            const int m = m0 + RPI * r + prow;
-            if (m >= g.m) continue;
-            const u32x4 s = staged(r);
-            uint8_t* yp = out(m);
-            if constexpr (RES == 0) {
-              if (y_st && n0 + EPL <= g.n) {
-                *reinterpret_cast<u32x4*>(yp) = s;
+            for (int r = 0; r < 32 / RPI; ++r) {
+              const u32x4 v = staged(r);
+              uint8_t* yp = y0 + (int64_t)r * RPI * g.ld_y * OSZ;
+              if (m0 + RPI * r >= g.m) continue;
+              if (vec && n0 + EPL <= g.n) {
+                *reinterpret_cast<u32x4*>(yp) = v;
               } else {
 #pragma unroll
                 for (int e = 0; e < EPL; ++e)
                   if (n0 + e < g.n) {
-                    if constexpr (SE == 2)
-                      reinterpret_cast<uint16_t*>(yp)[e] = (uint16_t)(s[e >> 1] >> (16 * (e & 1)));
-                    else
-                      reinterpret_cast<uint32_t*>(yp)[e] = s[e];
+                    if constexpr (OSZ == 2) reinterpret_cast<uint16_t*>(yp)[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+                    else reinterpret_cast<uint32_t*>(yp)[e] = v[e];
                   }
               }
-            } else {
-              f32x4 x = __builtin_bit_cast(f32x4, s);
-              if (f.gate != nullptr) gate_rows(m, x);
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (n0 + e < g.n) {
-                  if (f.residual != nullptr) x[e] += vec_elem(f.residual, RES == 1, (int64_t)m * f.ld_res + n0 + e);
-                  if constexpr (OUT == 1) reinterpret_cast<uint16_t*>(yp)[e] = (uint16_t)pack_bf16(x[e], 0.0f);
-                  else reinterpret_cast<float*>(yp)[e] = x[e];
-                }
             }
+          }
+        } else if constexpr (PIECES) {
+          // (whole loops under each branch: a branch per piece made every LDS read
+          // wait for its latency; 16384 x 3072 -> 12288 with a gate 386 -> 350 us)
+          constexpr int HR = 32 / RPI / (RES == 2 ? 2 : 1);   // fp32 residual: in halves (registers)
+#pragma unroll
+          for (int r0 = 0; r0 < 32 / RPI; r0 += HR) {
+            f32x4 x[HR];
+#pragma unroll
+            for (int r = 0; r < HR; ++r) x[r] = __builtin_bit_cast(f32x4, staged(r0 + r));
+            if (f.gate != nullptr) {
+#pragma unroll
+              for (int r = 0; r < HR; ++r) {
+                const bool second = m0 + RPI * (r0 + r) >= next;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[r][e] *= second ? gate[1][q][e] : gate[0][q][e];
+              }
+            }
+            if (f.residual != nullptr) {
+#pragma unroll
+              for (int r = 0; r < HR; ++r) {
+                const rvec rv = rres[p % RD][r0 + r];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if constexpr (RES == 1) x[r][e] += __uint_as_float(e & 1 ? rv[e >> 1] & 0xFFFF0000u : rv[e >> 1] << 16);
+                  else x[r][e] += __uint_as_float(rv[e]);
+                }
+              }
+            }
+#pragma unroll
+            for (int r = 0; r < HR; ++r) {
+              const int at = (int)offset(p, r0 + r, ldy, OSZ);
+              if constexpr (OUT == 1)
+                __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(x[r][0], x[r][1]), pack_bf16(x[r][2], x[r][3])},
+                                                      yr, at, 0, kNonTemporal);
+              else
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x[r]), yr, at, 0, kNonTemporal);
+            }
+          }
+        } else {   // element by element, bounds-checked (a rolled loop: little code)
+#pragma unroll 1
+          for (int r = 0; r < 32 / RPI; ++r) {
+            const f32x4 x = __builtin_bit_cast(f32x4, staged(r));
+            const int m = m0 + RPI * r;
+            if (m >= g.m) continue;
+            const int64_t ga = f.gate != nullptr ? (int64_t)((uint32_t)m / f.group_rows) * f.ld_gate : 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (n0 + e < g.n) {
+                float v = x[e];
+                if (f.gate != nullptr) v *= vec_elem(f.gate, f.vec_bf16, ga + n0 + e);
+                if (f.residual != nullptr) v += vec_elem(f.residual, f.res_bf16, (int64_t)m * f.ld_res + n0 + e);
+                const int64_t at = (int64_t)m * g.ld_y + n0 + e;
+                if constexpr (OUT == 1) static_cast<uint16_t*>(g.y)[at] = (uint16_t)pack_bf16(v, 0.0f);
+                else static_cast<float*>(g.y)[at] = v;
+              }
           }
         }
       }, std::make_integer_sequence<int, NP>{});
@@ -555,34 +665,57 @@ __global__ __launch_bounds__(NT, 1) void gemm_fused_large_kernel(FusedArgs f, in
   __builtin_amdgcn_s_waitcnt(0);
 }
 
-template <int ACT, int OUT, int RES, bool GLU>
-hipError_t launch_large(const FusedArgs& f, hipStream_t s) {
-  constexpr int TN = GLU ? BN / 2 : BN;
-  const int tiles_m = (f.g.m + BM - 1) / BM, tiles_n = (f.g.n + TN - 1) / TN;
-  const int grid = large_grid(tiles_m * tiles_n);
-  gemm_fused_large_kernel<ACT, OUT, RES, GLU><<<grid, NT, 0, s>>>(f, tiles_m, tiles_n, grid, (grid % 8) == 0);
+template <class T, int ACT, int OUT, int RES, bool GLU>
+hipError_t launch_tile(const FusedArgs& f, hipStream_t s) {
+  constexpr int TN = GLU ? T::BN / 2 : T::BN;
+  const int tiles_m = (f.g.m + T::BM - 1) / T::BM, tiles_n = (f.g.n + TN - 1) / TN;
+  const int grid = large_grid(tiles_m * tiles_n, T::WGS);
+  gemm_fused_large_kernel<T, ACT, OUT, RES, GLU><<<grid, T::NT, 0, s>>>(f, tiles_m, tiles_n, grid, (grid % 8) == 0);
   return hipGetLastError();
+}
+
+typedef Tile<256, 256, 4, 1> Large;
+typedef Tile<128, 128, 4, 2> Mid;
+
+template <int ACT, int OUT, int RES, bool GLU>
+hipError_t launch_large(const FusedArgs& f, bool mid, hipStream_t s) {
+  return mid ? launch_tile<Mid, ACT, OUT, RES, GLU>(f, s) : launch_tile<Large, ACT, OUT, RES, GLU>(f, s);
+}
+
+// What the kernels with RES 1 and 2 take: output and residual rows in whole
+// aligned pieces of 4 columns, byte offsets within a wave's rows below 2^31, and
+// gate groups of at least a wave's rows.
+inline bool whole_pieces(const FusedArgs& f, bool mid) {
+  auto ok = [&](const void* p, int64_t ld, int size) {
+    return (uintptr_t)p % (4 * size) == 0 && ld % 4 == 0 && ld * size * 128 < (int64_t(1) << 31);
+  };
+  const uint32_t wave_rows = (mid ? Mid::BM : Large::BM) / 2;
+  return f.g.n % 4 == 0 && ok(f.g.y, f.g.ld_y, f.g.y_bf16 ? 2 : 4) &&
+         (f.residual == nullptr || ok(f.residual, f.ld_res, f.res_bf16 ? 2 : 4)) &&
+         (f.gate == nullptr || f.group_rows >= wave_rows || f.group_rows >= (uint32_t)f.g.m);
 }
 
 // RES: a gate or a residual
 template <int ACT, bool GLU, bool RES>
-hipError_t launch_large_out(const FusedArgs& f, hipStream_t s) {
+hipError_t launch_large_out(const FusedArgs& f, bool mid, hipStream_t s) {
   if constexpr (RES) {
-    if (f.res_bf16) return f.g.y_bf16 ? launch_large<ACT, 1, 1, GLU>(f, s) : launch_large<ACT, 0, 1, GLU>(f, s);
-    return f.g.y_bf16 ? launch_large<ACT, 1, 2, GLU>(f, s) : launch_large<ACT, 0, 2, GLU>(f, s);
+    if (!whole_pieces(f, mid))
+      return f.g.y_bf16 ? launch_large<ACT, 1, 3, GLU>(f, mid, s) : launch_large<ACT, 0, 3, GLU>(f, mid, s);
+    if (f.residual == nullptr || f.res_bf16) return f.g.y_bf16 ? launch_large<ACT, 1, 1, GLU>(f, mid, s) : launch_large<ACT, 0, 1, GLU>(f, mid, s);
+    return f.g.y_bf16 ? launch_large<ACT, 1, 2, GLU>(f, mid, s) : launch_large<ACT, 0, 2, GLU>(f, mid, s);
   } else {
-    if (f.g.q_out) return launch_large<ACT, 2, 0, GLU>(f, s);
-    return f.g.y_bf16 ? launch_large<ACT, 1, 0, GLU>(f, s) : launch_large<ACT, 0, 0, GLU>(f, s);
+    if (f.g.q_out) return launch_large<ACT, 2, 0, GLU>(f, mid, s);
+    return f.g.y_bf16 ? launch_large<ACT, 1, 0, GLU>(f, mid, s) : launch_large<ACT, 0, 0, GLU>(f, mid, s);
   }
 }
 
 template <bool GLU, bool RES>
-hipError_t launch_large_act(const FusedArgs& f, hipStream_t s) {
+hipError_t launch_large_act(const FusedArgs& f, bool mid, hipStream_t s) {
   switch (f.act) {
-    case act::SILU: return launch_large_out<act::SILU, GLU, RES>(f, s);
-    case act::GELU: return launch_large_out<act::GELU, GLU, RES>(f, s);
-    case act::GELU_TANH: return launch_large_out<act::GELU_TANH, GLU, RES>(f, s);
-    default: return launch_large_out<A_LINEAR, GLU, RES>(f, s);
+    case act::SILU: return launch_large_out<act::SILU, GLU, RES>(f, mid, s);
+    case act::GELU: return launch_large_out<act::GELU, GLU, RES>(f, mid, s);
+    case act::GELU_TANH: return launch_large_out<act::GELU_TANH, GLU, RES>(f, mid, s);
+    default: return launch_large_out<A_LINEAR, GLU, RES>(f, mid, s);
   }
 }
 

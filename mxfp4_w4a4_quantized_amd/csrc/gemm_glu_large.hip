@@ -1,8 +1,10 @@
-// The large-tile gated GEMM (gemm_fused_large.h).
+// The tile kernels of the gated GEMM (gemm_fused_large.h).
 #include "gemm_fused_large.h"
 
 namespace mxfp4 {
 
-hipError_t launch_glu_large(const FusedArgs& f, hipStream_t s) { return large::launch_large_act<true, false>(f, s); }
+hipError_t launch_glu_tiles(const FusedArgs& f, bool mid, hipStream_t s) {
+  return large::launch_large_act<true, false>(f, mid, s);
+}
 
 }  // namespace mxfp4

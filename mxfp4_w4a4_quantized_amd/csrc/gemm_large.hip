@@ -519,9 +519,9 @@ int cu_count() {
   return n;
 }
 
-// Workgroups for ntiles output tiles.
-int large_grid(int ntiles) {
-  const int cus = cu_count();
+// Workgroups for ntiles output tiles, `per_cu` of them on a CU.
+int large_grid(int ntiles, int per_cu) {
+  const int cus = cu_count() * per_cu;
   int grid = ntiles < cus ? ntiles : cus;
   if (ntiles > cus) {
     // The rounds of tiles that one workgroup per CU needs, spread over the
@@ -547,7 +547,7 @@ bool gemm_large_supported(const GemmArgs& g) {
 hipError_t launch_gemm_large(const GemmArgs& g, hipStream_t s) {
   const int tiles_m = (g.m + BM - 1) / BM, tiles_n = (g.n + BN - 1) / BN;
   const int ntiles = tiles_m * tiles_n;
-  const int grid = large_grid(ntiles);
+  const int grid = large_grid(ntiles, 1);
   const int xcd_remap = (grid % 8) == 0;
   const size_t ybytes = g.y_bf16 ? 2 : 4;
   const int y_vec = (((uintptr_t)g.y) % (4 * ybytes) == 0) && (g.ld_y % 4 == 0);

@@ -58,7 +58,7 @@ int cu_count();
 bool gemm_large_supported(const GemmArgs& a);
 hipError_t launch_gemm_large(const GemmArgs& a, hipStream_t s);
 // Workgroups of the large-tile kernels for a number of output tiles.
-int large_grid(int ntiles);
+int large_grid(int ntiles, int per_cu);
 
 // Small-M kernel (gemm_small.hip): either layout; the kernel for decode
 // shapes (m <= 64), bound by streaming the weights from HBM, and for shapes
@@ -119,14 +119,13 @@ struct FusedArgs {
   bool h32 = false;
 };
 
-// The kernel for a call: small-M (decode shapes, few tiles, and row-major
-// operands that the large-tile kernel does not take), large-tile, or none.
-enum class FusedRoute { kSmall, kLarge, kNone };
+// The kernel for a call: small-M, 128 x 128 or 256 x 256 tiles, or none.
+enum class FusedRoute { kSmall, kMid, kLarge, kNone };
 FusedRoute fused_route(const FusedArgs& a);
 hipError_t launch_fused_small(const FusedArgs& a, hipStream_t s);
-hipError_t launch_fused_large(const FusedArgs& a, hipStream_t s);
-hipError_t launch_glu_large(const FusedArgs& a, hipStream_t s);        // its gated part
-hipError_t launch_residual_large(const FusedArgs& a, hipStream_t s);   // and that with a gate or a residual
+hipError_t launch_fused_tiles(const FusedArgs& a, bool mid, hipStream_t s);
+hipError_t launch_glu_tiles(const FusedArgs& a, bool mid, hipStream_t s);        // its gated part
+hipError_t launch_residual_tiles(const FusedArgs& a, bool mid, hipStream_t s);   // and that with a gate or a residual
 
 // Norm with residual, gate and modulation (norm.hip); dense or MXFP4 result.
 struct NormArgs {

@@ -54,13 +54,12 @@ def operand(rng, rows, k, e_lo, e_hi, layout):
 
 def act64(name, x):
     """act(x) in binary64 and the bound of the kernel's own error in it."""
-    from math import erfc
     if name == "none":
         return x, 0.0 * x
     if name == "relu":
         return np.maximum(x, 0.0), 0.0 * x
     if name == "gelu":
-        return x * 0.5 * np.vectorize(erfc)(-x / np.sqrt(2.0)), np.abs(x) * (0.75e-7 + 12 * U)
+        return x * 0.5 * torch.special.erfc(torch.from_numpy(-x / np.sqrt(2.0))).numpy(), np.abs(x) * (0.75e-7 + 12 * U)
     p = x if name == "silu" else 2 * np.sqrt(2 / np.pi) * (x + 0.044715 * x ** 3)
     y = x * np.where(p >= 0, 1 / (1 + np.exp(-np.abs(p))), np.exp(-np.abs(p)) / (1 + np.exp(-np.abs(p))))
     return y, (4 * 1.4427 * np.abs(p) + 10) * U * np.abs(y) + 1e-36
@@ -83,6 +82,7 @@ def preact(acc, absacc, bias, k):
 
 
 def absdot(ac, as_, bc, bs):
+    """|A| |B|^T"""
     return np.abs(oracle.dequantize(ac, as_)) @ np.abs(oracle.dequantize(bc, bs)).T
 
 
@@ -91,6 +91,9 @@ def absdot(ac, as_, bc, bs):
 SHAPES = [(1, 1, 32), (1, 256, 4096), (5, 40, 96), (16, 300, 512), (17, 96, 128), (33, 31, 160), (48, 64, 1024),
           (64, 128, 384), (65, 33, 96), (130, 520, 256), (300, 1000, 1184), (257, 259, 128), (520, 1030, 1152),
           (1100, 640, 256)]
+# shapes that the 128 x 128 and (the last) the 256 x 256 tile kernels take
+TILES = [(520, 8200, 256), (130, 9001, 512), (200, 4100, 4096), (770, 12850, 1280), (770, 12848, 1280)]
+GLU_TILES = [(520, 4100, 256), (130, 9001, 512), (770, 6425, 1280)]
 
 
 def vectors(gen, m, n, dtype):
@@ -101,7 +104,7 @@ def vectors(gen, m, n, dtype):
 
 
 @pytest.mark.parametrize("layout", [R, T])
-@pytest.mark.parametrize("m,n,k", SHAPES)
+@pytest.mark.parametrize("m,n,k", SHAPES + TILES)
 def test_epilogue(m, n, k, layout):
     if layout == T and k % 128:
         pytest.skip("tiled needs k % 128 == 0")
@@ -144,7 +147,7 @@ def test_epilogue(m, n, k, layout):
 
 
 @pytest.mark.parametrize("layout", [R, T])
-@pytest.mark.parametrize("m,n,k", SHAPES)
+@pytest.mark.parametrize("m,n,k", SHAPES + GLU_TILES)
 def test_glu(m, n, k, layout):
     if layout == T and k % 128:
         pytest.skip("tiled needs k % 128 == 0")
@@ -172,7 +175,8 @@ def test_glu(m, n, k, layout):
 
 
 QSHAPES = [(1, 32, 96), (16, 128, 4096), (20, 256, 256), (40, 384, 128), (64, 128, 640), (130, 96, 384),
-           (300, 640, 256), (1030, 768, 384), (1100, 640, 1184)]
+           (300, 640, 256), (1030, 768, 384), (1100, 640, 1184), (520, 8192, 256), (520, 4096, 256),
+           (770, 12800, 1280), (770, 6400, 1280)]
 
 
 @pytest.mark.parametrize("out_layout", [R, T])
@@ -210,7 +214,8 @@ def test_requant(m, n, k, layout, out_layout):
             assert np.array_equal(got[0], want[0]), f"{act} {rot} {glu}: {np.count_nonzero(got[0] != want[0])} codes"
 
 
-@pytest.mark.parametrize("m,n,k", [(3, 50, 256), (300, 522, 256), (600, 1024, 128), (1030, 768, 256)])
+@pytest.mark.parametrize("m,n,k", [(3, 50, 256), (300, 522, 256), (600, 1024, 128), (1030, 768, 256), (520, 8200, 256),
+                                   (770, 12852, 1280)])
 def test_strided_output_in_place_residual_and_guards(m, n, k):
     """Y and the residual are one strided buffer; what lies past column n stays."""
     for ld in (n + 6, n + 8, n + 1):
