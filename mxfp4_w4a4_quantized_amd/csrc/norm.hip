@@ -5,12 +5,14 @@
 // y dense, or quantized to MXFP4 after an optional block transform.
 //
 // Bound by HBM: x and the residual are read once, r and y (or 4.25 bits an
-// element of y) written once.  WPR waves own a row; every lane keeps its
+// element of y) written once (57344 x 3072, layer norm with gate and modulation:
+// 1.41 GB in 255 us, 5.5 TB/s; a large copy reaches 5.1-5.4).  A workgroup of 1
+// to 16 waves owns a row; every lane keeps its
 // columns of the row in registers as chunks of 8 consecutive elements (16
 // bytes of bf16: a wave's load instruction covers 1 KiB of the row), so the
 // statistics, which need the whole row, cost no second read.  Statistics are
-// fp32: per-lane sums, then a butterfly over the wave, then (WPR > 1) one LDS
-// exchange; the layer norm's variance is the mean square of the centred
+// fp32: per-lane sums, then a butterfly over the wave, then (several waves) one
+// LDS exchange; the layer norm's variance is the mean square of the centred
 // values, not a difference of moments.
 //
 // MXFP4 result: a 32-element block is four neighbouring lanes (a quad), so the
@@ -27,7 +29,10 @@ namespace {
 
 using namespace blockq;
 
+constexpr int MAXW = 16;   // waves per row at most
+
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   typedef float f2 __attribute__((ext_vector_type(2)));
@@ -37,20 +42,22 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 
 // Eight consecutive elements at column c of a row (columns past d read as 0;
 // VEC: whole aligned chunks).
-template <bool VEC>
+template <bool VEC, bool NT = false>
 __device__ __forceinline__ void load8(const void* base, bool bf16, int64_t off, uint32_t c, uint32_t d, float (&v)[8]) {
   if constexpr (VEC) {
     if (bf16) {
-      const u32x4 q = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + off + c);
+      const u32x4* qp = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + off + c);
+      const u32x4 q = NT ? __builtin_nontemporal_load(qp) : *qp;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         v[2 * j] = bf16_lo(q[j]);
         v[2 * j + 1] = bf16_hi(q[j]);
       }
     } else {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + off + c);
-      const float4 a = p[0], b = p[1];
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+      const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(base) + off + c);
+      const f32x4 a = NT ? __builtin_nontemporal_load(p) : p[0], b = NT ? __builtin_nontemporal_load(p + 1) : p[1];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
     }
   } else {
 #pragma unroll
@@ -63,16 +70,19 @@ __device__ __forceinline__ void load8(const void* base, bool bf16, int64_t off, 
   }
 }
 
-template <bool VEC>
+template <bool VEC, bool NT>
 __device__ __forceinline__ void store8(void* base, bool bf16, int64_t off, uint32_t c, uint32_t d, const float (&v)[8]) {
   if constexpr (VEC) {
     if (bf16) {
-      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(base) + off + c) =
-          u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+      u32x4* qp = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(base) + off + c);
+      const u32x4 q = u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+      if constexpr (NT) __builtin_nontemporal_store(q, qp);
+      else *qp = q;
     } else {
-      float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + off + c);
-      p[0] = make_float4(v[0], v[1], v[2], v[3]);
-      p[1] = make_float4(v[4], v[5], v[6], v[7]);
+      f32x4* p = reinterpret_cast<f32x4*>(static_cast<float*>(base) + off + c);
+      const f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+      if constexpr (NT) __builtin_nontemporal_store(a, p), __builtin_nontemporal_store(b, p + 1);
+      else p[0] = a, p[1] = b;
     }
   } else {
 #pragma unroll
@@ -91,26 +101,25 @@ __device__ __forceinline__ float quad_xor(float v) {
   return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), ctrl, 0xF, 0xF, true));
 }
 
-template <int WPR>
-__device__ __forceinline__ float row_sum(float v, float* slot, int wave) {
+__device__ __forceinline__ float row_sum(float v, float* slot, int wave, int waves) {
   v += quad_xor<1>(v);
   v += quad_xor<2>(v);
 #pragma unroll
   for (int o = 4; o < 64; o <<= 1) v += __shfl_xor(v, o);
-  if constexpr (WPR > 1) {
+  if (waves > 1) {
     if ((threadIdx.x & 63) == 0) slot[wave] = v;
     __syncthreads();
     v = slot[0];
-#pragma unroll
-    for (int i = 1; i < WPR; ++i) v += slot[i];
+    for (int i = 1; i < waves; ++i) v += slot[i];
   }
   return v;
 }
 
 // The scale of norm(v) over the row's d elements; centres v for a layer norm
 // (columns past d stay 0).
-template <int EPL, int WPR>
-__device__ __forceinline__ float statistics(const NormArgs& a, float (&v)[EPL][8], uint32_t c0, float* slots, int wave) {
+template <int EPL>
+__device__ __forceinline__ float statistics(const NormArgs& a, float (&v)[EPL][8], uint32_t c0, uint32_t step,
+                                            float* slots, int wave, int waves) {
   const float inv_d = 1.0f / (float)a.d;
   if (a.layer) {
     float s = 0.0f;
@@ -118,18 +127,18 @@ __device__ __forceinline__ float statistics(const NormArgs& a, float (&v)[EPL][8
     for (int i = 0; i < EPL; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) s += v[i][j];
-    const float mean = row_sum<WPR>(s, slots, wave) * inv_d;
+    const float mean = row_sum(s, slots, wave, waves) * inv_d;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = c0 + i * 512 * WPR + j < a.d ? v[i][j] - mean : 0.0f;
+      for (int j = 0; j < 8; ++j) v[i][j] = c0 + i * step + j < a.d ? v[i][j] - mean : 0.0f;
   }
   float q = 0.0f;
 #pragma unroll
   for (int i = 0; i < EPL; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) q = __builtin_fmaf(v[i][j], v[i][j], q);
-  return __builtin_amdgcn_rsqf(__builtin_fmaf(row_sum<WPR>(q, slots + WPR, wave), inv_d, a.eps));
+  return __builtin_amdgcn_rsqf(__builtin_fmaf(row_sum(q, slots + MAXW, wave, waves), inv_d, a.eps));
 }
 
 __device__ __forceinline__ int tiled_swz(int r) { return ((r >> 1) ^ (r >> 2)) & 3; }
@@ -264,18 +273,17 @@ __device__ __forceinline__ void kron_block(const NormArgs& a, const float* blk, 
 }
 
 // OUT: 0 dense y (or none), 1 MXFP4.  ROT as in block_quant.h; P x Q the
-// Kronecker factors.  A row's d columns are at most 512 WPR EPL.
-template <int WPR, int EPL, bool VEC, int OUT, int ROT, int P, int Q>
-__global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_kernel(NormArgs a) {
+// Kronecker factors, KD their columns in LDS.  EPL chunks of 8 columns per lane,
+// 512 EPL columns per wave.  NT: non-temporal loads and stores of whole rows.
+template <int EPL, bool VEC, bool NT, int OUT, int ROT, int P, int Q, int KD>
+__global__ __launch_bounds__(64 * MAXW) void norm_kernel(NormArgs a) {
   // Kronecker: the row, 36 words per 32-element block
-  __shared__ __attribute__((aligned(16))) float krow[ROT == 2 ? 16 * WPR * EPL * 36 : 1];
-  __shared__ float slots[4 * WPR];
+  __shared__ __attribute__((aligned(16))) float krow[KD / 32 * 36 + 1];
+  __shared__ float slots[4 * MAXW];
   const int lane = threadIdx.x & 63;
-  const int wave = WPR == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t row = WPR == 1 ? blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : blockIdx.x;
-  if (WPR == 1 && row >= a.rows) return;
-  const uint32_t c0 = 8 * (lane + 64 * wave);
-  constexpr uint32_t STEP = 512 * WPR;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const uint32_t row = blockIdx.x;
+  const uint32_t c0 = 8 * threadIdx.x, step = 512 * waves;
   const int64_t voff = (a.gate != nullptr || a.scale != nullptr || a.shift != nullptr)
                            ? (int64_t)(row / a.group_rows) * a.ld_vec
                            : 0;
@@ -283,17 +291,17 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_kernel(NormArg
   float v[EPL][8];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const uint32_t c = c0 + i * STEP;
-    if (c < a.d) load8<VEC>(a.x, a.x_bf16, (int64_t)row * a.ld_x, c, a.d, v[i]);
+    const uint32_t c = c0 + i * step;
+    if (c < a.d) load8<VEC, NT>(a.x, a.x_bf16, (int64_t)row * a.ld_x, c, a.d, v[i]);
     else
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
   }
   if (a.post_norm) {
-    const float inv = statistics<EPL, WPR>(a, v, c0, slots, wave);
+    const float inv = statistics<EPL>(a, v, c0, step, slots, wave, waves);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const uint32_t c = c0 + i * STEP;
+      const uint32_t c = c0 + i * step;
       if (c >= a.d) continue;
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[i][j] *= inv;
@@ -308,7 +316,7 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_kernel(NormArg
   if (a.gate != nullptr || a.residual != nullptr || a.residual_out != nullptr) {
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const uint32_t c = c0 + i * STEP;
+      const uint32_t c = c0 + i * step;
       if (c >= a.d) continue;
       if (a.gate != nullptr) {
         float w[8];
@@ -318,19 +326,19 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_kernel(NormArg
       }
       if (a.residual != nullptr) {
         float w[8];
-        load8<VEC>(a.residual, a.r_bf16, (int64_t)row * a.ld_r, c, a.d, w);
+        load8<VEC, NT>(a.residual, a.r_bf16, (int64_t)row * a.ld_r, c, a.d, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] = __builtin_fmaf(a.residual_scale, w[j], v[i][j]);
       }
-      if (a.residual_out != nullptr) store8<VEC>(a.residual_out, a.r_bf16, (int64_t)row * a.ld_ro, c, a.d, v[i]);
+      if (a.residual_out != nullptr) store8<VEC, NT>(a.residual_out, a.r_bf16, (int64_t)row * a.ld_ro, c, a.d, v[i]);
     }
   }
   if (OUT == 0 && a.y == nullptr) return;
 
-  const float inv = statistics<EPL, WPR>(a, v, c0, slots + 2 * WPR, wave);
+  const float inv = statistics<EPL>(a, v, c0, step, slots + 2 * MAXW, wave, waves);
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const uint32_t c = c0 + i * STEP;
+    const uint32_t c = c0 + i * step;
     // a lane past the row's end has no quad partner inside it (d % 32 == 0)
     if (c < a.d) {
 #pragma unroll
@@ -361,7 +369,7 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_kernel(NormArg
       }
     }
     if constexpr (OUT == 0) {
-      if (c < a.d) store8<VEC>(a.y, a.y_bf16, (int64_t)row * a.ld_y, c, a.d, v[i]);
+      if (c < a.d) store8<VEC, NT>(a.y, a.y_bf16, (int64_t)row * a.ld_y, c, a.d, v[i]);
     } else if constexpr (ROT != 2) {
       if (c < a.d) quantize_quad<ROT>(a, v[i], row, c, lane);
     } else {
@@ -375,46 +383,59 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_kernel(NormArg
   if constexpr (OUT == 1 && ROT == 2) {
     __syncthreads();
     const uint32_t nblk = a.d >> 5;
-    constexpr uint32_t PER = 64 * WPR / Q;   // blocks a pass
-    for (uint32_t b0 = 0; b0 < nblk; b0 += PER) {
+    const uint32_t per = blockDim.x / Q;   // blocks a pass
+    for (uint32_t b0 = 0; b0 < nblk; b0 += per) {
       const uint32_t b = b0 + threadIdx.x / Q;
       if (b < nblk) kron_block<P, Q>(a, krow + b * 36, row, b, lane % Q);   // whole groups of Q lanes
     }
   }
 }
 
-template <int WPR, int EPL, bool VEC, int OUT, int ROT, int P = 1, int Q = 32>
+template <int EPL, bool VEC, bool NT, int OUT, int ROT, int P = 1, int Q = 32, int KD = 0>
 void run(const NormArgs& a, hipStream_t s) {
-  const uint32_t grid = WPR == 1 ? (a.rows + 3) / 4 : a.rows;
-  norm_kernel<WPR, EPL, VEC, OUT, ROT, P, Q><<<grid, WPR == 1 ? 256 : 64 * WPR, 0, s>>>(a);
+  const uint32_t waves = (a.d + 512 * EPL - 1) / (512 * EPL);
+  norm_kernel<EPL, VEC, NT, OUT, ROT, P, Q, KD><<<a.rows, 64 * waves, 0, s>>>(a);
 }
 
-// A row's registers: 4 waves up to 16384 columns, 16 waves up to 65536.
-template <bool VEC, int OUT, int ROT>
+// Chunks per lane.  Few rows (two workgroups per CU): one, the most waves and
+// the shortest row latency (16 x 4096: 3.4 us against 4.0 with two).  More: two,
+// which ask for twice the bytes per wave before the first barrier (57344 x 3072
+// with modulation 255 us against 318).  Rows past two chunks on 16 waves: eight.
+// Either way a row takes as many waves as it has whole 512-column chunks for:
+// with four waves always, 3072 columns left half of the second chunk idle (301).
+template <bool VEC, bool NT, int OUT, int ROT>
 void run_width(const NormArgs& a, hipStream_t s) {
-  if (a.d <= 2048) run<4, 1, VEC, OUT, ROT>(a, s);
-  else if (a.d <= 4096) run<4, 2, VEC, OUT, ROT>(a, s);
-  else if (a.d <= 8192) run<4, 4, VEC, OUT, ROT>(a, s);
-  else if (a.d <= 16384) run<4, 8, VEC, OUT, ROT>(a, s);
-  else run<16, 8, VEC, OUT, ROT>(a, s);
+  if (a.d <= 8192 && a.rows <= 2u * (uint32_t)cu_count()) run<1, VEC, NT, OUT, ROT>(a, s);
+  else if (a.d <= 16384) run<2, VEC, NT, OUT, ROT>(a, s);
+  else run<8, VEC, NT, OUT, ROT>(a, s);
+}
+
+// Inputs larger than the 256 MB last-level cache stream past it (263 -> 253 us
+// at 57344 x 3072); smaller ones, which the kernel before has just written,
+// are read through it (777 x 5120: 12.6 us against 15.5).
+template <bool VEC, int OUT, int ROT>
+void run_size(const NormArgs& a, hipStream_t s) {
+  const uint64_t elem = (a.x_bf16 ? 2 : 4) + (a.residual == nullptr ? 0 : a.r_bf16 ? 2 : 4);
+  if (a.rows * elem * a.d > (uint64_t(256) << 20)) run_width<VEC, true, OUT, ROT>(a, s);
+  else run_width<VEC, false, OUT, ROT>(a, s);
 }
 
 template <int P, int Q>
 void run_kron(const NormArgs& a, hipStream_t s) {
-  if (a.d <= 4096) run<4, 2, true, 1, 2, P, Q>(a, s);
-  else run<4, 8, true, 1, 2, P, Q>(a, s);
+  if (a.d <= 4096) run<2, true, false, 1, 2, P, Q, 4096>(a, s);
+  else run<2, true, false, 1, 2, P, Q, kNormMaxDKron>(a, s);
 }
 
 hipError_t dispatch(const NormArgs& a, hipStream_t s) {
   if (a.codes == nullptr) {
-    if (a.vec) run_width<true, 0, 0>(a, s);
-    else run_width<false, 0, 0>(a, s);
+    if (a.vec) run_size<true, 0, 0>(a, s);
+    else run_width<false, false, 0, 0>(a, s);
     return hipGetLastError();
   }
   switch (a.rot) {
-    case 0: run_width<true, 1, 0>(a, s); break;
-    case 1: run_width<true, 1, 1>(a, s); break;
-    case 3: run_width<true, 1, 3>(a, s); break;
+    case 0: run_size<true, 1, 0>(a, s); break;
+    case 1: run_size<true, 1, 1>(a, s); break;
+    case 3: run_size<true, 1, 3>(a, s); break;
     default:
       switch (a.p) {
         case 1: run_kron<1, 32>(a, s); break;
