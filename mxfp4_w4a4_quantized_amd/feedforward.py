@@ -21,8 +21,8 @@ from typing import Optional
 
 import torch
 
-from . import (HADAMARD32, MXFP4_BF16, MXFP4_F32, ROT_HADAMARD32, ROWMAJOR, RotationDesc, _check, _out_shapes,
-               _rot_desc, lib)
+from . import (HADAMARD32, MXFP4_BF16, MXFP4_F32, ROT_HADAMARD32, ROWMAJOR, TILED, RotationDesc, _check,
+               _out_shapes, _rot_desc, lib, padded_rows)
 
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 NORM_KINDS = {"rms": 0, "layer": 1}
@@ -403,14 +403,44 @@ def ffn(x, p: Norm, residual, w_up, w_down, hidden: int, w_gate=None, act="silu"
     `rot` (None or "h32"); gate: [groups, d], by p.group_rows.  Returns (y, r),
     r the residual stream between the norm and the block (x where there is no
     residual add)."""
+    # the calls of norm_quantize, gemm_glu_requant / gemm_epilogue_requant and
+    # gemm_epilogue, with the intermediates in one allocation and not checked
+    # again: a decode step's kernels take 30 us, as long as the three bindings
+    desc, r, dev = _norm_desc(x, p, residual, None)
     rows, d = x.shape
-    codes, scales, r = norm_quantize(x, p, residual, rot, layout)
-    if w_gate is not None:
-        h = gemm_glu_requant(codes, scales, *w_gate, *w_up, act=act, bias_g=bias_gate, bias_u=bias_up, rot=rot,
-                             layout=layout, out_layout=layout, m=rows, n=hidden)
-    else:
-        h = gemm_epilogue_requant(codes, scales, *w_up, Epilogue(act=act, bias=bias_up), rot=rot, layout=layout,
-                                  out_layout=layout, m=rows, n=hidden)
     r = x if r is None else r
-    e = Epilogue(bias=bias_down, gate=gate, group_rows=p.group_rows, residual=r)
-    return gemm_epilogue(*h, *w_down, e, out_dtype=r.dtype, y=y, layout=layout, m=rows, n=d), r
+    if rot is not None and rot != HADAMARD32:
+        raise ValueError("rot must be None or \"h32\" (the transform is also that of the hidden activations)")
+    rdesc = None if rot is None else _H32
+    down = _packed("w_down", *w_down, d, hidden, layout, dev)
+    if w_gate is not None:
+        glu = _glu_desc(act, *w_gate, *w_up, bias_gate, bias_up, hidden, d, layout, dev)
+    else:
+        if bias_gate is not None:
+            raise ValueError("bias_gate needs w_gate")
+        up = _packed("w_up", *w_up, hidden, d, layout, dev)
+        e_up = _epilogue_desc(Epilogue(act=act, bias=bias_up), rows, hidden, dev)
+    e_down = _epilogue_desc(Epilogue(bias=bias_down, gate=gate, group_rows=p.group_rows, residual=r), rows, d, dev)
+    y, yp, ld, yt = _dense_output(y, rows, d, r.dtype, x)
+    if rows == 0:
+        return y, r
+    rp = padded_rows(rows) if layout == TILED else rows
+    sizes = [rp * d // 2, rp * d // 32, rp * hidden // 2, rp * hidden // 32]
+    starts, total = [], 0
+    for size in sizes:
+        starts.append(total)
+        total += (size + 255) // 256 * 256
+    work = torch.empty(total, dtype=torch.uint8, device=x.device)
+    base = work.data_ptr()
+    xc, xs, hc, hs = (base + at for at in starts)
+    L, stream = lib(), _raw_stream(dev)
+    _check(L.mxfp4_norm_quantize(desc, rdesc, layout, xc, xs, stream), "mxfp4_norm_quantize")
+    if w_gate is not None:
+        _check(L.mxfp4_gemm_glu_requant(xc, xs, rows, glu, hidden, d, layout, rdesc, hc, hs, layout, stream),
+               "mxfp4_gemm_glu_requant")
+    else:
+        _check(L.mxfp4_gemm_epilogue_requant(xc, xs, rows, *up, hidden, d, layout, e_up, rdesc, hc, hs, layout, stream),
+               "mxfp4_gemm_epilogue_requant")
+    _check(L.mxfp4_gemm_epilogue(hc, hs, rows, *down, d, hidden, layout, e_down, yp, yt, ld, stream),
+           "mxfp4_gemm_epilogue")
+    return y, r

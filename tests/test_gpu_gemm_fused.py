@@ -297,6 +297,36 @@ def test_side_stream_and_graph_replays():
         assert all(torch.equal(a, b) for a, b in zip(got, want)), i
 
 
+def test_ffn_row_major_without_residual_and_empty():
+    d, f, m = 96, 160, 9
+    gen = torch.Generator().manual_seed(3)
+    w = [mx.quantize_weight((torch.randn(*s, generator=gen) * 0.05).to(DEV)) for s in ((f, d), (f, d), (d, f))]
+    x = torch.randn(m, d, generator=gen).to(BF).to(DEV)
+    bias = [torch.randn(n, generator=gen).to(BF).to(DEV) for n in (f, f, d)]
+    p = mx.Norm(kind="layer")
+    announce("ffn row-major, no residual add before the norm")
+    for gated in (False, True):
+        kw = dict(w_gate=w[1], bias_gate=bias[1]) if gated else {}
+        y, r = mx.ffn(x, p, None, w[0], w[2], f, act="silu", bias_up=bias[0], bias_down=bias[2], **kw)
+        c, s, r2 = mx.norm_quantize(x, p)
+        assert r2 is None
+        if gated:
+            h = mx.gemm_glu_requant(c, s, *w[1], *w[0], act="silu", bias_g=bias[1], bias_u=bias[0])
+        else:
+            h = mx.gemm_epilogue_requant(c, s, *w[0], mx.Epilogue(act="silu", bias=bias[0]))
+        want = mx.gemm_epilogue(*h, *w[2], mx.Epilogue(bias=bias[2], residual=x))
+        torch.cuda.synchronize()
+        assert torch.equal(r, x) and torch.equal(y, want)
+    y, r = mx.ffn(x[:0], p, None, w[0], w[2], f)
+    assert y.shape == (0, d) and r.shape == (0, d)
+    with pytest.raises(ValueError):
+        mx.ffn(x, p, None, w[0], w[2], f, bias_gate=bias[1])
+    with pytest.raises(ValueError):
+        mx.ffn(x, p, None, w[2], w[2], f)
+    with pytest.raises(ValueError):
+        mx.ffn(x, p, None, w[0], w[2], f, rot=mx.Smooth(torch.ones(d, device=DEV)))
+
+
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("m", [1, 16, 70, 1100])
 def test_ffn_equals_its_parts(m, gated):
