@@ -6,12 +6,12 @@
 //
 // Bound by HBM: x and the residual are read once, r and y (or 4.25 bits an
 // element of y) written once (57344 x 3072, layer norm with gate and modulation:
-// 1.41 GB in 255 us, 5.5 TB/s; a large copy reaches 5.1-5.4).  A workgroup of 1
-// to 16 waves owns a row; every lane keeps its
-// columns of the row in registers as chunks of 8 consecutive elements (16
-// bytes of bf16: a wave's load instruction covers 1 KiB of the row), so the
-// statistics, which need the whole row, cost no second read.  Statistics are
-// fp32: per-lane sums, then a butterfly over the wave, then (several waves) one
+// 1.41 GB in 243 us, 5.8 TB/s; a large copy reaches 5.1-5.4).  A workgroup of 1
+// to 16 waves owns a row; every lane keeps its columns of the row in registers
+// as chunks of 8 consecutive elements (16 bytes of bf16: a wave's load
+// instruction covers 1 KiB of the row), so the statistics, which need the whole
+// row, cost no second read.  Statistics are fp32: per-lane sums, then the wave's
+// sum by lane permutes, then (several waves) one
 // LDS exchange; the layer norm's variance is the mean square of the centred
 // values, not a difference of moments.
 //
@@ -40,19 +40,44 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, b2));
 }
 
-// Eight consecutive elements at column c of a row (columns past d read as 0;
+// Eight consecutive elements at column c of a row as they lie in memory: one
+// 16-byte piece of bf16 or two of fp32.
+template <bool NT>
+__device__ __forceinline__ void raw8(const void* base, bool bf16, int64_t off, uint32_t c, u32x4 (&q)[2]) {
+  const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(base) + (off + c) * (bf16 ? 2 : 4));
+  q[0] = NT ? __builtin_nontemporal_load(p) : p[0];
+  if (!bf16) q[1] = NT ? __builtin_nontemporal_load(p + 1) : p[1];
+}
+
+__device__ __forceinline__ u32x4 vec8(const void* base, int64_t off, uint32_t c) {
+  return *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + off + c);
+}
+
+__device__ __forceinline__ void widen(u32x4 q, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = bf16_lo(q[j]);
+    v[2 * j + 1] = bf16_hi(q[j]);
+  }
+}
+
+__device__ __forceinline__ void widen8(const u32x4 (&q)[2], bool bf16, float (&v)[8]) {
+  if (bf16) {
+    widen(q[0], v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(q[j >> 2][j & 3]);
+  }
+}
+
+// The same, widened (columns past d read as 0;
 // VEC: whole aligned chunks).
 template <bool VEC, bool NT = false>
 __device__ __forceinline__ void load8(const void* base, bool bf16, int64_t off, uint32_t c, uint32_t d, float (&v)[8]) {
   if constexpr (VEC) {
     if (bf16) {
       const u32x4* qp = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + off + c);
-      const u32x4 q = NT ? __builtin_nontemporal_load(qp) : *qp;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[2 * j] = bf16_lo(q[j]);
-        v[2 * j + 1] = bf16_hi(q[j]);
-      }
+      widen(NT ? __builtin_nontemporal_load(qp) : *qp, v);
     } else {
       const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(base) + off + c);
       const f32x4 a = NT ? __builtin_nontemporal_load(p) : p[0], b = NT ? __builtin_nontemporal_load(p + 1) : p[1];
@@ -104,8 +129,13 @@ __device__ __forceinline__ float quad_xor(float v) {
 __device__ __forceinline__ float row_sum(float v, float* slot, int wave, int waves) {
   v += quad_xor<1>(v);
   v += quad_xor<2>(v);
-#pragma unroll
-  for (int o = 4; o < 64; o <<= 1) v += __shfl_xor(v, o);
+  v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x141, 0xF, 0xF, true));   // row_half_mirror
+  v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x140, 0xF, 0xF, true));   // row_mirror
+  // both results hold v's even and odd 16-lane rows, then its lower and upper halves
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(h[0]) + __uint_as_float(h[1]);
   if (waves > 1) {
     if ((threadIdx.x & 63) == 0) slot[wave] = v;
     __syncthreads();
@@ -117,7 +147,7 @@ __device__ __forceinline__ float row_sum(float v, float* slot, int wave, int wav
 
 // The scale of norm(v) over the row's d elements; centres v for a layer norm
 // (columns past d stay 0).
-template <int EPL>
+template <int EPL, bool VEC>
 __device__ __forceinline__ float statistics(const NormArgs& a, float (&v)[EPL][8], uint32_t c0, uint32_t step,
                                             float* slots, int wave, int waves) {
   const float inv_d = 1.0f / (float)a.d;
@@ -131,7 +161,7 @@ __device__ __forceinline__ float statistics(const NormArgs& a, float (&v)[EPL][8
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = c0 + i * step + j < a.d ? v[i][j] - mean : 0.0f;
+      for (int j = 0; j < 8; ++j) v[i][j] = c0 + i * step + (VEC ? 0 : j) < a.d ? v[i][j] - mean : 0.0f;
   }
   float q = 0.0f;
 #pragma unroll
@@ -282,23 +312,48 @@ __global__ __launch_bounds__(64 * MAXW) void norm_kernel(NormArgs a) {
   __shared__ float slots[4 * MAXW];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
-  const uint32_t row = blockIdx.x;
+  // Tiled codes of 16 rows share cache lines, and workgroup i runs on XCD i % 8,
+  // each with its own L2: an XCD takes 32 neighbouring rows of 256 (57344 x 3072
+  // with modulation, H32: 162 us against 167).
+  uint32_t row = blockIdx.x;
+  if (OUT == 1 && a.tiled && (row | 255u) < a.rows) row = (row & ~255u) + 32 * (row & 7) + ((row >> 3) & 31);
   const uint32_t c0 = 8 * threadIdx.x, step = 512 * waves;
   const int64_t voff = (a.gate != nullptr || a.scale != nullptr || a.shift != nullptr)
                            ? (int64_t)(row / a.group_rows) * a.ld_vec
                            : 0;
 
+  // All of x's chunks are in flight before the first is widened.
+  constexpr bool AHEAD = VEC && EPL <= 2;
+  const bool ahead = AHEAD && a.vec_bf16;
+  constexpr int PE = AHEAD ? EPL : 1;
+  u32x4 xq[PE][2], last[4][PE];
+  if constexpr (AHEAD) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const uint32_t c = c0 + i * step;
+      if (c < a.d) raw8<NT>(a.x, a.x_bf16, (int64_t)row * a.ld_x, c, xq[i]);
+    }
+  }
+  auto vec = [&](int which, const void* base, int64_t off, int i, uint32_t c, float (&w)[8]) {
+    if (AHEAD && ahead) widen(last[which][AHEAD ? i : 0], w);
+    else load8<VEC>(base, a.vec_bf16, off, c, a.d, w);
+  };
+
   float v[EPL][8];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const uint32_t c = c0 + i * step;
-    if (c < a.d) load8<VEC, NT>(a.x, a.x_bf16, (int64_t)row * a.ld_x, c, a.d, v[i]);
-    else
+    if (c >= a.d) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+    } else if constexpr (AHEAD) {
+      widen8(xq[i], a.x_bf16, v[i]);
+    } else {
+      load8<VEC, NT>(a.x, a.x_bf16, (int64_t)row * a.ld_x, c, a.d, v[i]);
+    }
   }
   if (a.post_norm) {
-    const float inv = statistics<EPL>(a, v, c0, step, slots, wave, waves);
+    const float inv = statistics<EPL, VEC>(a, v, c0, step, slots, wave, waves);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
       const uint32_t c = c0 + i * step;
@@ -335,7 +390,23 @@ __global__ __launch_bounds__(64 * MAXW) void norm_kernel(NormArgs a) {
   }
   if (OUT == 0 && a.y == nullptr) return;
 
-  const float inv = statistics<EPL>(a, v, c0, step, slots + 2 * MAXW, wave, waves);
+  // The last step's vectors are asked for before the statistics' barriers: an
+  // L2 round trip for all of them, hidden, instead of one each behind the
+  // barriers (57344 x 3072 with modulation to bf16: 132 us against 161, together
+  // with x's chunks above).  Asked for with x they would take the registers of
+  // a resident workgroup (173 us).
+  if constexpr (AHEAD) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const uint32_t c = c0 + i * step;
+      if (!ahead || c >= a.d) continue;
+      if (a.weight != nullptr) last[0][i] = vec8(a.weight, 0, c);
+      if (a.bias != nullptr) last[1][i] = vec8(a.bias, 0, c);
+      if (a.scale != nullptr) last[2][i] = vec8(a.scale, voff, c);
+      if (a.shift != nullptr) last[3][i] = vec8(a.shift, voff, c);
+    }
+  }
+  const float inv = statistics<EPL, VEC>(a, v, c0, step, slots + 2 * MAXW, wave, waves);
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const uint32_t c = c0 + i * step;
@@ -345,25 +416,25 @@ __global__ __launch_bounds__(64 * MAXW) void norm_kernel(NormArgs a) {
       for (int j = 0; j < 8; ++j) v[i][j] *= inv;
       if (a.weight != nullptr) {
         float w[8];
-        load8<VEC>(a.weight, a.vec_bf16, 0, c, a.d, w);
+        vec(0, a.weight, 0, i, c, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] *= w[j];
       }
       if (a.bias != nullptr) {
         float w[8];
-        load8<VEC>(a.bias, a.vec_bf16, 0, c, a.d, w);
+        vec(1, a.bias, 0, i, c, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] += w[j];
       }
       if (a.scale != nullptr) {
         float w[8];
-        load8<VEC>(a.scale, a.vec_bf16, voff, c, a.d, w);
+        vec(2, a.scale, voff, i, c, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] *= 1.0f + w[j];
       }
       if (a.shift != nullptr) {
         float w[8];
-        load8<VEC>(a.shift, a.vec_bf16, voff, c, a.d, w);
+        vec(3, a.shift, voff, i, c, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] += w[j];
       }
@@ -398,9 +469,10 @@ void run(const NormArgs& a, hipStream_t s) {
 }
 
 // Chunks per lane.  Few rows (two workgroups per CU): one, the most waves and
-// the shortest row latency (16 x 4096: 3.4 us against 4.0 with two).  More: two,
-// which ask for twice the bytes per wave before the first barrier (57344 x 3072
-// with modulation 255 us against 318).  Rows past two chunks on 16 waves: eight.
+// the shortest row latency (16 x 4096: 3.4 us against 4.0 with two; 3.1 since
+// the last step's vectors are read ahead).  More: two, which ask for twice the
+// bytes per wave before the first barrier (57344 x 3072 with modulation 255 us
+// against 318; 243 since then).  Rows past two chunks on 16 waves: eight.
 // Either way a row takes as many waves as it has whole 512-column chunks for:
 // with four waves always, 3072 columns left half of the second chunk idle (301).
 template <bool VEC, bool NT, int OUT, int ROT>
