@@ -449,7 +449,9 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(FusedAr
           float am = 0.0f;
 #pragma unroll
           for (int r = 0; r < 16; ++r) am = fmaxf(am, fabsf(v[r]));
-          am = fmaxf(am, __shfl_xor(am, 32));
+          float other = am;
+          swap_halves(am, other);   // both lanes of a row: its lower and its upper half's
+          am = fmaxf(am, other);
           const uint32_t ef = __float_as_uint(am) >> 23;
           const uint32_t sb = ef > 2u ? ef - 2u : 0u;
           const float sc = __uint_as_float(sb ? sb << 23 : 0x00400000u);
@@ -463,8 +465,8 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(FusedAr
           w1 = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w1, v[12], v[13], sc, 2);
           w1 = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w1, v[14], v[15], sc, 3);
           // half 0 collects code bytes 0..7 of the block, half 1 bytes 8..15
-          const uint32_t recv = (uint32_t)__shfl_xor((int)(lg ? w0 : w1), 32);
-          const uint32_t lo = lg ? recv : w0, hi = lg ? w1 : recv;
+          const auto lh = __builtin_amdgcn_permlane32_swap(w0, w1, false, false);
+          const uint32_t lo = lh[0], hi = lh[1];
           const uint32_t d0 = (lo & 0xFFFFu) | (hi << 16), d1 = (lo >> 16) | (hi & 0xFFFF0000u);
           if (row_ok && nw0 + 32 * o < g.n) {
             const int chunk = g.q_tiled ? (blk0 + o) ^ swr : o;

@@ -201,25 +201,38 @@ __device__ __forceinline__ void finish(const FusedArgs& f, const Extra<GLU> (&e)
   }
 }
 
+// One butterfly between neighbouring lane groups, of X lanes, for two registers
+// at once: a permlane swap, [a0 a1] [b0 b1] -> [a0 b0] [a1 b1], makes it one
+// add and one subtract, and is its own inverse.
+template <int X>
+__device__ __forceinline__ void butterfly_lanes(float& a, float& b) {
+  auto swap = [](float p, float q) {
+    if constexpr (X == 16) return __builtin_amdgcn_permlane16_swap(__float_as_uint(p), __float_as_uint(q), false, false);
+    else return __builtin_amdgcn_permlane32_swap(__float_as_uint(p), __float_as_uint(q), false, false);
+  };
+  const auto r = swap(a, b);
+  const float u = __uint_as_float(r[0]), w = __uint_as_float(r[1]);
+  const auto t = swap(u + w, u - w);
+  a = __uint_as_float(t[0]);
+  b = __uint_as_float(t[1]);
+}
+
 // Hadamard-32 of the 32-column block of each row: lane (r, g) holds columns
 // 4g + j (v0) and 16 + 4g + j (v1).  Butterflies with strides 1, 2, 4, 8, 16
 // and the final multiply in the quantizer's order: strides 1 and 2 run over j,
-// 4 and 8 over the lane groups (the upper lane forms u - w from its partner's
-// u), 16 over v0 and v1.
-__device__ __forceinline__ void hadamard_lanes(v4f& v0, v4f& v1, int lane) {
+// 4 and 8 over the lane groups, 16 over v0 and v1.
+__device__ __forceinline__ void hadamard_lanes(v4f& v0, v4f& v1) {
   v4f* v[2] = {&v0, &v1};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    v4f& t = *v[h];
+    const v4f t = *v[h];
     const float a0 = t[0] + t[1], a1 = t[0] - t[1], a2 = t[2] + t[3], a3 = t[2] - t[3];
-    t = v4f{a0 + a2, a1 + a3, a0 - a2, a1 - a3};
-#pragma unroll
-    for (int x = 16; x <= 32; x <<= 1)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float o = __shfl_xor(t[r], x);
-        t[r] = (lane & x) ? o - t[r] : t[r] + o;
-      }
+    float b[4] = {a0 + a2, a1 + a3, a0 - a2, a1 - a3};
+    butterfly_lanes<16>(b[0], b[1]);
+    butterfly_lanes<16>(b[2], b[3]);
+    butterfly_lanes<32>(b[0], b[1]);
+    butterfly_lanes<32>(b[2], b[3]);
+    *v[h] = v4f{b[0], b[1], b[2], b[3]};
   }
   const float c = __uint_as_float(0x3E3504F3u);   // nearest fp32 to 1/sqrt(32)
 #pragma unroll
@@ -336,7 +349,7 @@ __global__ __launch_bounds__(64 * MAXW) void gemm_fused_small_kernel(FusedArgs f
     finish<GLU>(f, e, v, u);
     const int m = m0 + 16 * mg + lr;
     if constexpr (OUT == 2) {
-      if (f.h32) hadamard_lanes(v[0], v[1], lane);
+      if (f.h32) hadamard_lanes(v[0], v[1]);
       store_requant(g, m, n0, v[0], v[1], lane);
     } else {
       const int n = n0 + 16 * p + 4 * lg;
