@@ -31,7 +31,8 @@
 // (bf16, H32 where MXFP4; the GEMM without an epilogue in brackets):
 //  * 57344 x 3072 -> 12288, bias, tanh GELU   1147-1263 us, 3.4-3.8 PF/s (1018)
 //  * 8192 x 4096 -> 2 x 14336, gated silu      441-477 us, 4.0-4.4 PF/s (434)
-//  * 3584 x 12288 -> 3072, bias, gate, residual 80-83 us, 3.3-3.4 PF/s (69.5)
+//  * 3584 x 12288 -> 3072, bias, gate, residual 78-83 us, 3.3-3.5 PF/s (69.5)
+//  * 3584 x 3072 -> 12288, tanh GELU, H32, MXFP4  95 us, 2.8 PF/s (72.6)
 //  * 523 x 1408 -> 2 x 3001 fp32, gated, bias      12 us (128 x 128 tiles)
 #pragma once
 #include "gemm_large_core.h"
