@@ -136,6 +136,7 @@ struct NormArgs {
   const void *gate, *scale, *shift;           // [groups][ld_vec]
   int64_t ld_x, ld_r, ld_ro, ld_vec;
   uint32_t rows, d, group_rows;
+  uint32_t row0 = 0;                          // first row of the launch
   bool x_bf16, r_bf16, vec_bf16;
   bool layer, post_norm;
   bool vec;                                   // every pointer and stride 16-byte aligned, d % 8 == 0

@@ -24,6 +24,8 @@
 #include "internal.h"
 #include "block_quant.h"
 
+#include <algorithm>
+
 namespace mxfp4 {
 namespace {
 
@@ -315,7 +317,7 @@ __global__ __launch_bounds__(64 * MAXW) void norm_kernel(NormArgs a) {
   // Tiled codes of 16 rows share cache lines, and workgroup i runs on XCD i % 8,
   // each with its own L2: an XCD takes 32 neighbouring rows of 256 (57344 x 3072
   // with modulation, H32: 162 us against 167).
-  uint32_t row = blockIdx.x;
+  uint32_t row = a.row0 + blockIdx.x;
   if (OUT == 1 && a.tiled && (row | 255u) < a.rows) row = (row & ~255u) + 32 * (row & 7) + ((row >> 3) & 31);
   const uint32_t c0 = 8 * threadIdx.x, step = 512 * waves;
   const int64_t voff = (a.gate != nullptr || a.scale != nullptr || a.shift != nullptr)
@@ -465,7 +467,14 @@ __global__ __launch_bounds__(64 * MAXW) void norm_kernel(NormArgs a) {
 template <int EPL, bool VEC, bool NT, int OUT, int ROT, int P = 1, int Q = 32, int KD = 0>
 void run(const NormArgs& a, hipStream_t s) {
   const uint32_t waves = (a.d + 512 * EPL - 1) / (512 * EPL);
-  norm_kernel<EPL, VEC, NT, OUT, ROT, P, Q, KD><<<a.rows, 64 * waves, 0, s>>>(a);
+  // A grid holds fewer than 2^32 threads: more rows take several launches, of
+  // whole groups of 256 rows.
+  const uint32_t per = 0xFFFFFFFFu / (64 * waves) & ~255u;
+  for (uint32_t row0 = 0; row0 < a.rows; row0 += per) {
+    NormArgs b = a;
+    b.row0 = row0;
+    norm_kernel<EPL, VEC, NT, OUT, ROT, P, Q, KD><<<std::min(per, a.rows - row0), 64 * waves, 0, s>>>(b);
+  }
 }
 
 // Chunks per lane.  Few rows (two workgroups per CU): one, the most waves and

@@ -225,3 +225,23 @@ def test_empty_nan_and_extreme_rows():
     assert torch.isnan(y[2, 4]) and bool((y[2, :4] == 0).all())       # 1 / infinity elsewhere
     assert bool((y[3] == 0).all())
     assert float((y[0] - 1).abs().max()) <= 1e-6
+
+
+def test_more_rows_than_one_grid_holds():
+    """64 threads a row: 2^26 rows pass the 2^32 threads of a launch."""
+    rows, d, tail = (1 << 26) + 300, 32, 600
+    x = torch.zeros(rows, d, dtype=BF, device=DEV)
+    last = rand(torch.Generator().manual_seed(8), tail, d, dtype=BF, std=2.0)
+    x[-tail:] = last.to(DEV)
+    p = mx.Norm(kind="rms")
+    announce("norm of 2^26 + 300 rows")
+    y = torch.full((rows, d), 3.0, dtype=BF, device=DEV)
+    mx.norm(x, p, y=y)
+    codes, scales, _ = mx.norm_quantize(x, p, None, "h32")
+    torch.cuda.synchronize()
+    want, _, by, _ = reference(x[-tail:], p, None)
+    check(y[-tail:], want, by, "y")
+    assert float(y[:-tail].abs().amax()) == 0.0
+    y32, _ = mx.norm(x[-tail:].contiguous(), p, out_dtype=F)
+    wc, ws = mx.quantize_rotate(y32, "h32")
+    assert torch.equal(codes[-tail:], wc) and torch.equal(scales[-tail:], ws)
