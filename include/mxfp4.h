@@ -347,7 +347,10 @@ typedef enum {
 } mxfp4_act;
 
 /* Statistics of a norm: RMS  z = r / sqrt(mean(r^2) + eps);
- * LAYER  z = (r - mean(r)) / sqrt(mean((r - mean(r))^2) + eps). */
+ * LAYER  z = (r - mean(r)) / sqrt(mean((r - mean(r))^2) + eps).
+ * Any finite eps >= 0.  Rows whose mean square leaves fp32's range are scaled by
+ * a power of two first, so z is right for them too (a row of zeros with eps = 0
+ * gives NaN, as 0 / 0).  For LAYER the row's sum has to be finite in fp32. */
 typedef enum {
     MXFP4_NORM_RMS = 0,
     MXFP4_NORM_LAYER = 1

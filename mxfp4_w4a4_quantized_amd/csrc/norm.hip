@@ -147,30 +147,63 @@ __device__ __forceinline__ float row_sum(float v, float* slot, int wave, int wav
   return v;
 }
 
-// The scale of norm(v) over the row's d elements; centres v for a layer norm
-// (columns past d stay 0).
+// v minus the row's mean (columns past d stay 0).
 template <int EPL, bool VEC>
-__device__ __forceinline__ float statistics(const NormArgs& a, float (&v)[EPL][8], uint32_t c0, uint32_t step,
-                                            float* slots, int wave, int waves) {
-  const float inv_d = 1.0f / (float)a.d;
-  if (a.layer) {
-    float s = 0.0f;
+__device__ __forceinline__ void centre(const NormArgs& a, float (&v)[EPL][8], uint32_t c0, uint32_t step, float inv_d,
+                                       float* slots, int wave, int waves) {
+  float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
+  for (int i = 0; i < EPL; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s += v[i][j];
-    const float mean = row_sum(s, slots, wave, waves) * inv_d;
+    for (int j = 0; j < 8; ++j) s += v[i][j];
+  const float mean = row_sum(s, slots, wave, waves) * inv_d;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
+  for (int i = 0; i < EPL; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = c0 + i * step + (VEC ? 0 : j) < a.d ? v[i][j] - mean : 0.0f;
-  }
+    for (int j = 0; j < 8; ++j) v[i][j] = c0 + i * step + (VEC ? 0 : j) < a.d ? v[i][j] - mean : 0.0f;
+}
+
+// mean(v^2) + eps
+template <int EPL>
+__device__ __forceinline__ float mean_square(const float (&v)[EPL][8], float inv_d, float eps, float* slots, int wave,
+                                             int waves) {
   float q = 0.0f;
 #pragma unroll
   for (int i = 0; i < EPL; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) q = __builtin_fmaf(v[i][j], v[i][j], q);
-  return __builtin_amdgcn_rsqf(__builtin_fmaf(row_sum(q, slots + MAXW, wave, waves), inv_d, a.eps));
+  return __builtin_fmaf(row_sum(q, slots, wave, waves), inv_d, eps);
+}
+
+// The scale of norm(v) over the row's d elements; centres v for a layer norm.
+//
+// The mean square of fp32 values leaves fp32's range long before they do, and
+// v_rsq_f32 takes subnormal arguments as 0.  Where it falls below 2^-100 (only
+// with eps below that; down to there underflow costs its squares nothing) or
+// overflows, the row is scaled by 2^100 or 2^-100, centred again (the first mean
+// was rounded to a multiple of 2^-149) and squared anew: 2^-149 <= |v| < 2^-42
+// gives squares in [2^-98, 2^116], |v| < 2^128 squares below 2^56.  What is
+// returned is then the scale of the scaled row.  Every lane holds the same sum,
+// so a workgroup's waves take the same way.  (A block of its own: as a second
+// pass of a loop it took 13 more registers and spilled long rows.)
+template <int EPL, bool VEC>
+__device__ __forceinline__ float statistics(const NormArgs& a, float (&v)[EPL][8], uint32_t c0, uint32_t step,
+                                            float* slots, int wave, int waves) {
+  const float inv_d = 1.0f / (float)a.d;
+  if (a.layer) centre<EPL, VEC>(a, v, c0, step, inv_d, slots, wave, waves);
+  float ms = mean_square(v, inv_d, a.eps, slots + MAXW, wave, waves);
+  const float t = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(ms)));
+  if (__builtin_expect(t < 0x1p-100f || t == __builtin_inff(), 0)) {
+    const float s = t < 1.0f ? 0x1p100f : 0x1p-100f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] *= s;
+    if (waves > 1) __syncthreads();   // the slots have been read
+    if (a.layer) centre<EPL, VEC>(a, v, c0, step, inv_d, slots, wave, waves);
+    ms = mean_square(v, inv_d, a.eps * s * s, slots + MAXW, wave, waves);
+  }
+  return __builtin_amdgcn_rsqf(ms);
 }
 
 __device__ __forceinline__ int tiled_swz(int r) { return ((r >> 1) ^ (r >> 2)) & 3; }
