@@ -6,12 +6,15 @@
 // The main loop is gemm_large.hip's (its header describes it): persistent
 // 4-wave workgroups on 256 x 256 tiles, a 4-stage LDS ring of direct loads that
 // runs across tile boundaries, 128 x 128 accumulators per wave.  What differs:
-//  * Bias.  The accumulators of a tile start from the bias instead of zero, on
-//    the matrix pipe: one v_mfma_f32_32x32x2_f32 per fragment, bias values of
-//    the fragment's 32 weight rows (K index 0) against ones, writes bias[row]
-//    into all 16 registers (exact: one product and zeros).  It takes the place
-//    of the MFMA that clears a fragment, so a bias costs four dword loads per
-//    wave and tile.
+//  * Bias.  It is added to the finished sums, so that a bias far above them
+//    costs one rounding and not one per K step, and on the matrix pipe: one
+//    v_mfma_f32_32x32x2_f32 per fragment, bias values of the fragment's 32
+//    weight rows (K index 0) against ones, adds bias[row] to all 16 registers.
+//    It runs one fragment ahead of the epilogue's vector work.  An fp32 MFMA
+//    still holds that up for its 64 cycles (57344 x 3072 -> 12288, tanh GELU:
+//    23 us in 1255), so the accumulators are cleared by a bf16 one, which does
+//    not (their start from the bias, by an fp32 MFMA too, took as long as now:
+//    1271 and 1275 us).
 //  * Gated form.  A tile is 256 weight rows that alternate 32 rows of G and the
 //    matching 32 rows of U, so a wave's even fragments hold the gate's
 //    pre-activations and the odd ones the up projection's, for the same
@@ -97,11 +100,21 @@ __device__ __forceinline__ void each(F&& body, std::integer_sequence<int, I...>)
   (body(std::integral_constant<int, I>{}), ...);
 }
 
-// acc[i][j] = bias of weight row i, for every j.  The s_nop and the wait
-// states at the tile start are those of acc_zero_mfma.
-__device__ __forceinline__ void acc_bias_mfma(v16f& acc, float bias, float one) {
-  asm volatile("s_nop 2\n\tv_mfma_f32_32x32x2_f32 %0, %1, %2, 0" : "=a"(acc) : "v"(bias), "v"(one));
+// acc = 0, by a product of zeros (bf16: two operand registers).  The s_nop and
+// the wait states at the tile start are those of acc_zero_mfma.
+__device__ __forceinline__ void acc_clear(v16f& acc, uint64_t zero) {
+  asm volatile("s_nop 2\n\tv_mfma_f32_32x32x8_bf16 %0, %1, %1, 0" : "=a"(acc) : "v"(zero));
 }
+
+// acc[i][j] += bias of weight row i, for every j: one product and a zero, one
+// rounding.  The compiler does not know it for an MFMA: the last MFMA before it
+// that wrote acc, and the first read of acc after it, have to be 19 wait states
+// (16 passes) away.
+__device__ __forceinline__ void acc_add_bias(v16f& acc, float bias, float one) {
+  asm volatile("s_nop 2\n\tv_mfma_f32_32x32x2_f32 %0, %1, %2, %0" : "+a"(acc) : "v"(bias), "v"(one));
+}
+
+__device__ __forceinline__ void mfma_wait() { asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory"); }
 
 __device__ __forceinline__ float vec_elem(const void* p, bool bf16, int64_t i) {
   if (bf16) return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
@@ -287,14 +300,15 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(FusedAr
       xf[q] = *reinterpret_cast<const u32x4*>(sbuf + xrow[q] * RB + 16 * (c ^ swz(xrow[q])));
   };
 
-  // Bias of this lane's weight row in each fragment of the wave, for this
-  // workgroup's j-th tile (lanes 32-63 feed the MFMA's second K index: 0).
+  // Bias of this lane's weight row in each fragment of the wave (lanes 32-63
+  // feed the MFMA's second K index: 0).
   float one;
+  uint64_t zero = 0;
   asm volatile("v_mov_b32 %0, 1.0" : "=v"(one));
+  asm volatile("" : "+v"(zero));
+  const bool biased = f.bias != nullptr || (GLU && f.bias_u != nullptr);
   float bias[FN];
-  auto load_bias = [&](int j) {
-    int tm, tn;
-    tile_coords(j * grid + slot, tiles_m, tiles_n, tm, tn);
+  auto load_bias = [&](int tn) {
 #pragma unroll
     for (int a = 0; a < FN; ++a) {
       const void* src = GLU && (a & 1) ? f.bias_u : f.bias;
@@ -312,11 +326,10 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(FusedAr
     issue_scales();
   }
   v16f acc[FN][FM];
-  load_bias(0);
 #pragma unroll
   for (int a = 0; a < FN; ++a)
 #pragma unroll
-    for (int c = 0; c < FM; ++c) acc_bias_mfma(acc[a][c], bias[a], one);
+    for (int c = 0; c < FM; ++c) acc_clear(acc[a][c], zero);
 
   wait_stages<NBUF - 2, LPS>();
   __builtin_amdgcn_s_barrier();
@@ -350,9 +363,10 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(FusedAr
     int tm, tn;
     tile_coords(j * grid + slot, tiles_m, tiles_n, tm, tn);
     const int ahead = AHEAD && f.residual != nullptr ? max(nk - PF, 0) : nk;
-    // the compiler does not see the accumulators' start values being written
-    // (inline asm): wait states before the K loop's MFMAs read them
-    asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+    if (biased) load_bias(tn);
+    // the compiler does not see the accumulators being cleared (inline asm):
+    // wait states before the K loop's MFMAs read them
+    mfma_wait();
 
     for (int kt = 0; kt < nk; ++kt) {
       if constexpr (AHEAD) {
@@ -395,31 +409,48 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(FusedAr
 
     // ---- epilogue of this workgroup's j-th tile
     const int mw0 = tm * BM + wm * (BM / WM), nw0 = tn * TN + wn * WCOLS;   // the wave's block of Y
-    if ((j + 1) * nk < total) load_bias(j + 1);   // the next tile's start values
     const bool relu = f.act == act::RELU;
+    constexpr int NO = GLU ? FN / 2 : FN;   // output fragments along N
 
+    // The bias onto the i-th output fragment, in the order in which they leave.
+    auto add_bias = [&](int i) {
+      const int o = i % NO, bb = i / NO;
+      if constexpr (GLU) {
+        acc_add_bias(acc[2 * o][bb], bias[2 * o], one);
+        acc_add_bias(acc[2 * o + 1][bb], bias[2 * o + 1], one);
+      } else {
+        acc_add_bias(acc[o][bb], bias[o], one);
+      }
+    };
+    if (biased) {
+      mfma_wait();
+      add_bias(0);
+      mfma_wait();
+    }
     // Output fragment `o` (of FN, or FN / 2 gated ones) for activation rows
-    // bb: accumulators read, their next start values written, act applied.
+    // bb: accumulators read and cleared, act applied.  The next one's bias is
+    // added first: the 16 reads, the wait and the clearing MFMA that follow are
+    // the wait states until that one is read.
     auto take = [&](int o, int bb, float (&v)[16]) {
+      if (biased && bb * NO + o + 1 < NO * FM) add_bias(bb * NO + o + 1);
       if constexpr (GLU) {
         float u[16];
 #pragma unroll
         for (int r = 0; r < 16; ++r) v[r] = acc_read(acc[2 * o][bb][r]);
-        acc_bias_mfma(acc[2 * o][bb], bias[2 * o], one);
+        acc_clear(acc[2 * o][bb], zero);
 #pragma unroll
         for (int r = 0; r < 16; ++r) u[r] = acc_read(acc[2 * o + 1][bb][r]);
-        acc_bias_mfma(acc[2 * o + 1][bb], bias[2 * o + 1], one);
+        acc_clear(acc[2 * o + 1][bb], zero);
         activate<ACT>(v, relu);
 #pragma unroll
         for (int r = 0; r < 16; ++r) v[r] = v[r] * u[r];
       } else {
 #pragma unroll
         for (int r = 0; r < 16; ++r) v[r] = acc_read(acc[o][bb][r]);
-        acc_bias_mfma(acc[o][bb], bias[o], one);
+        acc_clear(acc[o][bb], zero);
         activate<ACT>(v, relu);
       }
     };
-    constexpr int NO = GLU ? FN / 2 : FN;   // output fragments along N
 
     if constexpr (OUT == 2) {
       // MXFP4 output from the registers: lane l (row l % 32, half g = l / 32)
