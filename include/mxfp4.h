@@ -335,8 +335,8 @@ MXFP4_API mxfp4_status mxfp4_smooth_weight_factors(const float* r, int64_t k, fl
  * NaN and infinities as the formulas do; MXFP4 outputs are defined for finite
  * values.  The library is inference only: no gradients. */
 
-/* Activations.  GELU uses the Abramowitz and Stegun 7.1.26 rational
- * approximation of erf (absolute error below 1.5e-7); GELU_TANH is
+/* Activations.  GELU is x Phi(x) (the erf form), off by at most
+ * (45 + 1.5 x^2) 2^-24 of the result also in the negative tail; GELU_TANH is
  * x * sigmoid(2 sqrt(2/pi) (x + 0.044715 x^3)), the tanh form. */
 typedef enum {
     MXFP4_ACT_NONE = 0,

@@ -6,9 +6,14 @@
 //   silu(x)      = x / (1 + 2^(-log2(e) x))
 //   gelu_tanh(x) = 0.5 x (1 + tanh(u)) = x sigmoid(2 u),
 //                  2 u = 2 sqrt(2/pi) (x + 0.044715 x^3)
-//   gelu(x)      = x Phi(x), Phi by Abramowitz and Stegun 7.1.26: for z >= 0
-//                  erfc(z) = t (a1 + t (a2 + t (a3 + t (a4 + t a5)))) e^(-z^2),
-//                  t = 1 / (1 + 0.3275911 z), absolute error below 1.5e-7
+//   gelu(x)      = x Phi(x), Phi(-a) = t poly(t) e^(-a^2 / 2) for a >= 0 with
+//                  t = 1 / (1 + 0.295 a): a polynomial of degree 7 fitted to
+//                  Phi(-a) e^(a^2 / 2) / t for a <= 13.5 (in 64 bits, by least
+//                  squares reweighted towards the largest error, in units of
+//                  (3 + 1.25 a^2) 2^-24 of the value, what rounding the exponent
+//                  costs).  The tail keeps its relative accuracy, (45 + 1.5 x^2)
+//                  2^-24 at most; the last factor is the exponential, which stays
+//                  normal as long as the result does.
 // At infinities and NaN they follow the formulas: the exponential saturates to
 // 0 or infinity, and act(-inf) is -inf * 0 = NaN.
 #pragma once
@@ -38,15 +43,21 @@ __device__ __forceinline__ float gelu_tanh(float x) {
 }
 
 __device__ __forceinline__ float gelu(float x) {
-  const float ax = fabsf(x);
-  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(ax, 0.231641888f, 1.0f));   // 0.3275911 / sqrt(2)
-  // the coefficients halved: p e = erfc(|x| / sqrt(2)) / 2 = Phi(-|x|)
-  float p = __builtin_fmaf(t, 0.5307027145f, -0.7265760135f);
-  p = __builtin_fmaf(t, p, 0.7107068705f);
-  p = __builtin_fmaf(t, p, -0.142248368f);
-  p = __builtin_fmaf(t, p, 0.127414796f);
-  const float q = p * t * __builtin_amdgcn_exp2f(x * x * -0.7213475204f);   // e^(-x^2 / 2)
-  return x * (x < 0.0f ? q : 1.0f - q);
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(fabsf(x), 0.295f, 1.0f));
+  float p = __builtin_fmaf(t, 0.0373435728f, -0.173062041f);
+  p = __builtin_fmaf(t, p, 0.249138921f);
+  p = __builtin_fmaf(t, p, -0.0914765298f);
+  p = __builtin_fmaf(t, p, 0.148233667f);
+  p = __builtin_fmaf(t, p, 0.0925811902f);
+  p = __builtin_fmaf(t, p, 0.119663447f);
+  p = __builtin_fmaf(t, p, 0.117577776f);
+  const float e = __builtin_amdgcn_exp2f(x * x * -0.7213475204f);   // e^(-x^2 / 2); NaN stays NaN
+  // s e = x Phi(-|x|), in s with x at most 2^100 (so that it is 0 at infinity);
+  // then x Phi(x) = max(x, 0) - |s e|.  Both limits on x's bits: as floats each
+  // would cost the compiler an instruction more for signalling NaN.
+  const int i = __float_as_int(x);
+  const float s = __int_as_float(min(i, 0x71800000)) * (p * t);
+  return __builtin_fmaf(-fabsf(s), e, __int_as_float(max(i, 0)));
 }
 
 }  // namespace act

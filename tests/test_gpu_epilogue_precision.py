@@ -47,3 +47,46 @@ def test_bias_is_added_to_the_finished_sum(m, n, k, layout):
     within(h, want, 3.01 * U * np.abs(want), "gated, both biases")
     want = acc * x[1]
     within(one, want, 2.01 * U * np.abs(want), "gated, up bias")
+
+
+def activation(act, x, m, glu=False):
+    """act of the values x [n] through the epilogue of an m-row GEMM: zero
+    products, x as the bias (fp32 result, every row alike).  glu: through the
+    gated form, times an up projection of 1."""
+    n, k = x.numel(), 256
+    a = torch.zeros(m, k // 2, dtype=torch.uint8, device=DEV), torch.full((m, k // 32), 127, dtype=torch.uint8, device=DEV)
+    b = torch.zeros(n, k // 2, dtype=torch.uint8, device=DEV), torch.full((n, k // 32), 127, dtype=torch.uint8, device=DEV)
+    x = x.to(DEV)
+    if glu:
+        y = mx.gemm_glu(*a, *b, *b, act, x, torch.ones(n, device=DEV), F)
+    else:
+        y = mx.gemm_epilogue(*a, *b, mx.Epilogue(act=act, bias=x), F)
+    torch.cuda.synchronize()
+    same = (y == y[:1]) | (torch.isnan(y) & torch.isnan(y[:1]))
+    assert bool(same.all())
+    return y[0].cpu()
+
+
+# rows and columns that take the small-M, the 128 x 128 and the 256 x 256 tile kernels
+ROUTES = [(3, 1000), (130, 9000), (770, 12800)]
+
+
+def test_gelu_keeps_the_tail():
+    """gelu(x) = x Phi(x) relative to the result, through the negative tail.
+    x Phi(-|x|) is x t poly(t) 2^(c x^2), t = 1 / (1 + p |x|), p = 0.285:
+      fit 3 u, coefficients 1 u; t 3 u, times |d ln Phi(-a) e^(a^2/2) / d ln t|
+      <= 0.8 / p: 9 u; Horner's 8 steps, 2 u each of sums of positive and
+      negative terms at most 1.4 times the value: 23 u; the products t poly, x q,
+      q E 3 u; the exponent 2.5 u of x^2 / 2 (its square, its product, its
+      constant) and v_exp_f32 2 u: 41 u + 1.25 x^2 u.
+    For x > 0, x - that: at most as much and 2 u.  Bound (45 + 1.5 x^2) u.  The
+    exponential flushes below 2^-126, where the result is below 0.4 2^-126."""
+    for m, n in ROUTES:
+        x = torch.cat([torch.linspace(-13.3, 8, n - 6), torch.tensor([0.0, -0.0, 1e-30, -1e-30, 40.0, 1e30])])
+        v = x.double()
+        want = (v * 0.5 * torch.special.erfc(-v / np.sqrt(2.0))).numpy()
+        bound = (45 + 1.5 * v.numpy() ** 2) * U * np.abs(want) + 2.0 ** -127
+        bound[-1] = U * 1e30
+        for glu in (False, True):
+            announce("gelu", m, n, glu)
+            within(activation("gelu", x, m, glu), want, bound, f"gelu {m} {glu}")
