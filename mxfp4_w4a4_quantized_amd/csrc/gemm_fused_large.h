@@ -77,19 +77,26 @@ __device__ __forceinline__ void load_lds4(const uint8_t* src, uint8_t* dst) {
   __builtin_amdgcn_global_load_lds(src, dst, 4, 0, 0);
 }
 
-// Activation classes of the kernels that apply it in registers.
+// Activation classes of the kernels that apply it in registers, to W values of a
+// fragment at a time.
 constexpr int A_LINEAR = 0;   // none or relu, by f.act
-template <int ACT>
+template <int ACT, int W>
 __device__ __forceinline__ void activate(float (&v)[16], bool relu) {
   if constexpr (ACT == A_LINEAR) {
-    if (relu) {
-#pragma unroll
-      for (int r = 0; r < 16; ++r) v[r] = act::relu(v[r]);
-    }
+    if (relu) act::relu(v);
+  } else if constexpr (ACT == act::GELU) {
+    act::gelu(v);
   } else {
 #pragma unroll
-    for (int r = 0; r < 16; ++r)
-      v[r] = ACT == act::SILU ? act::silu(v[r]) : ACT == act::GELU ? act::gelu(v[r]) : act::gelu_tanh(v[r]);
+    for (int h = 0; h < 16; h += W) {
+      float x[W];
+#pragma unroll
+      for (int r = 0; r < W; ++r) x[r] = v[h + r];
+      if constexpr (ACT == act::SILU) act::silu(x);
+      else act::gelu_tanh(x);
+#pragma unroll
+      for (int r = 0; r < W; ++r) v[h + r] = x[r];
+    }
   }
 }
 
@@ -427,6 +434,10 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(FusedAr
       add_bias(0);
       mfma_wait();
     }
+    // Values that an activation takes together: a branch for each group, so all
+    // of a fragment's, but 4 beside an fp32 residual's pieces, whose kernels are
+    // at the limit of their registers (with 16 at a time four of them spilled).
+    constexpr int AW = RES == 2 ? 4 : 16;
     // Output fragment `o` (of FN, or FN / 2 gated ones) for activation rows
     // bb: accumulators read and cleared, act applied.  The next one's bias is
     // added first: the 16 reads, the wait and the clearing MFMA that follow are
@@ -441,14 +452,14 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(FusedAr
 #pragma unroll
         for (int r = 0; r < 16; ++r) u[r] = acc_read(acc[2 * o + 1][bb][r]);
         acc_clear(acc[2 * o + 1][bb], zero);
-        activate<ACT>(v, relu);
+        activate<ACT, AW>(v, relu);
 #pragma unroll
         for (int r = 0; r < 16; ++r) v[r] = v[r] * u[r];
       } else {
 #pragma unroll
         for (int r = 0; r < 16; ++r) v[r] = acc_read(acc[o][bb][r]);
         acc_clear(acc[o][bb], zero);
-        activate<ACT>(v, relu);
+        activate<ACT, AW>(v, relu);
       }
     };
 

@@ -159,19 +159,18 @@ __device__ __forceinline__ void load_extra(const FusedArgs& f, int m, int n, Ext
 // act on every value, chosen once
 template <int N>
 __device__ __forceinline__ void activate(int kind, v4f (&v)[N]) {
-  auto apply = [&](auto fn) __attribute__((always_inline)) {
+  float x[4 * N];
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) v[i][r] = fn(v[i][r]);
-  };
+  for (int i = 0; i < 4 * N; ++i) x[i] = v[i / 4][i % 4];
   switch (kind) {
-    case act::RELU: apply([](float x) __attribute__((always_inline)) { return act::relu(x); }); break;
-    case act::SILU: apply([](float x) __attribute__((always_inline)) { return act::silu(x); }); break;
-    case act::GELU: apply([](float x) __attribute__((always_inline)) { return act::gelu(x); }); break;
-    case act::GELU_TANH: apply([](float x) __attribute__((always_inline)) { return act::gelu_tanh(x); }); break;
+    case act::RELU: act::relu(x); break;
+    case act::SILU: act::silu(x); break;
+    case act::GELU: act::gelu(x); break;
+    case act::GELU_TANH: act::gelu_tanh(x); break;
     default: break;
   }
+#pragma unroll
+  for (int i = 0; i < 4 * N; ++i) v[i / 4][i % 4] = x[i];
 }
 
 // The epilogue of N fragments of a lane: v their sums (u: the up projection's).

@@ -90,3 +90,28 @@ def test_gelu_keeps_the_tail():
         for glu in (False, True):
             announce("gelu", m, n, glu)
             within(activation("gelu", x, m, glu), want, bound, f"gelu {m} {glu}")
+
+
+def quotient64(act, x):
+    """x / (1 + 2^t) in 64 bits, and |t|."""
+    p = x if act == "silu" else 2 * np.sqrt(2 / np.pi) * (x + 0.044715 * x ** 3)
+    q = np.exp(-np.abs(p))
+    return x * np.where(p >= 0, 1 / (1 + q), q / (1 + q)), np.abs(p) * 1.4426950408889634
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_silu_and_tanh_gelu_over_the_range_of_fp32(act):
+    """Relative to the result wherever that is normal: t carries 4 roundings,
+    times ln 2 in the exponential, v_exp_f32 and v_rcp_f32 2 u each, the sum and
+    the products 6 u: (4 |t| + 10) u, as test_gpu_gemm_fused.py has it, here
+    with no absolute part but the spacing of subnormal results, 2^-149."""
+    for m, n in ROUTES:
+        lo = -92.0 if act == "silu" else -10.2
+        tiny = torch.tensor([s * f * 2.0 ** e for e in range(-126, -90, 3) for s in (1, -1) for f in (1.0, 1.4, 1.9)])
+        ends = torch.tensor([lo + 3.2, lo + 0.5, lo, -88.8 if act == "silu" else -9.95, 2.0 ** 100, 3e38, -3e38, 0.0])
+        x = torch.cat([tiny, ends, torch.linspace(lo, 9, n - tiny.numel() - ends.numel())])
+        want, t = quotient64(act, x.double().numpy())
+        bound = (4 * np.minimum(t, 200) + 10) * U * np.abs(want) + 2.0 ** -149
+        for glu in (False, True):
+            announce(act, m, n, glu)
+            within(activation(act, x, m, glu), want, bound, f"{act} {m} {glu}")
