@@ -137,7 +137,7 @@ def _matrix(name, t, shape, dev):
     rows, cols = shape
     if col != 1 and cols != 1:
         raise _bad(name, t, shape, dev)
-    return t.data_ptr(), ld if rows > 1 or ld > cols else cols
+    return t.data_ptr(), ld if rows > 1 else cols
 
 
 def _grouped(name, t, shape, dtype, dev):
@@ -148,6 +148,9 @@ def _grouped(name, t, shape, dtype, dev):
     return ptr, t.dtype, ld
 
 
+# Layout of a result like x: by itself empty_like takes over the row stride of a
+# view of one row.
+_ROWS = torch.contiguous_format
 _CODES = {torch.float32: MXFP4_F32, torch.bfloat16: MXFP4_BF16}
 
 
@@ -195,7 +198,7 @@ def _norm_desc(x, p, residual, residual_out):
     if residual is not None or residual_out is not None or p.gate is not None or p.post_norm:
         like = x if residual is None else residual
         if residual_out is None:
-            residual_out = torch.empty_like(like)
+            residual_out = torch.empty_like(like, memory_format=_ROWS)
         elif residual is not None and residual_out.dtype != residual.dtype:
             raise ValueError(f"residual_out is {residual_out.dtype}, residual {residual.dtype}")
         out, ld_ro = _matrix("residual_out", residual_out, shape, dev)
@@ -234,7 +237,7 @@ def norm(x, p: Norm, residual=None, out_dtype=None, y=None, residual_out=None):
     residual_out may be `residual`, which then holds r."""
     desc, r, dev = _norm_desc(x, p, residual, residual_out)
     if y is None:
-        y = torch.empty_like(x, dtype=out_dtype)
+        y = torch.empty_like(x, dtype=out_dtype, memory_format=_ROWS)
     ptr, ld = _matrix("y", y, x.shape, dev)
     _check(lib().mxfp4_norm(desc, ptr, _code(y.dtype), ld, _raw_stream(dev)), "mxfp4_norm")
     return y, r
