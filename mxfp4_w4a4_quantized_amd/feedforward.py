@@ -55,6 +55,17 @@ class GluDesc(ctypes.Structure):
 # .cuda_stream gives the same through a Stream object, which costs 1.7 us more
 # on each call.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _stream(dev):
+    """The current stream of GPU dev.  The handle of a default stream is 0 for
+    every GPU, and a launch on it goes to the current one."""
+    stream = _raw_stream(dev)
+    if stream == 0 and _current_device() != dev:
+        raise ValueError(f"the operands are on GPU {dev}, whose default stream needs it as the current device "
+                         f"(torch.cuda.device({dev}))")
+    return stream
 
 
 def declare(L):
@@ -239,7 +250,7 @@ def norm(x, p: Norm, residual=None, out_dtype=None, y=None, residual_out=None):
     if y is None:
         y = torch.empty_like(x, dtype=out_dtype, memory_format=_ROWS)
     ptr, ld = _matrix("y", y, x.shape, dev)
-    _check(lib().mxfp4_norm(desc, ptr, _code(y.dtype), ld, _raw_stream(dev)), "mxfp4_norm")
+    _check(lib().mxfp4_norm(desc, ptr, _code(y.dtype), ld, _stream(dev)), "mxfp4_norm")
     return y, r
 
 
@@ -282,7 +293,7 @@ def norm_quantize(x, p: Norm, residual=None, rot=None, layout: int = ROWMAJOR, c
     rows, d = x.shape
     codes, scales, cp, sp = _packed_outputs(rows, d, layout, codes, scales, x)
     rdesc, _keep = _rotation(rot, x, d)
-    _check(lib().mxfp4_norm_quantize(desc, rdesc, layout, cp, sp, _raw_stream(dev)), "mxfp4_norm_quantize")
+    _check(lib().mxfp4_norm_quantize(desc, rdesc, layout, cp, sp, _stream(dev)), "mxfp4_norm_quantize")
     return codes, scales, r
 
 
@@ -335,7 +346,7 @@ def gemm_epilogue(a_codes, a_scales, b_codes, b_scales, e: Epilogue = None, out_
     bc, bs = _packed("operand B", b_codes, b_scales, n, k, layout, dev)
     desc = _epilogue_desc(e, m, n, dev)
     y, ptr, ld, yt = _dense_output(y, m, n, out_dtype, a_codes)
-    _check(lib().mxfp4_gemm_epilogue(ac, as_, m, bc, bs, n, k, layout, desc, ptr, yt, ld, _raw_stream(dev)),
+    _check(lib().mxfp4_gemm_epilogue(ac, as_, m, bc, bs, n, k, layout, desc, ptr, yt, ld, _stream(dev)),
            "mxfp4_gemm_epilogue")
     return y
 
@@ -351,7 +362,7 @@ def gemm_epilogue_requant(a_codes, a_scales, b_codes, b_scales, e: Epilogue = No
     rdesc, _keep = _rotation(rot, a_codes, n)
     y_codes, y_scales, yc, ys = _packed_outputs(m, n, out_layout, y_codes, y_scales, a_codes)
     _check(lib().mxfp4_gemm_epilogue_requant(ac, as_, m, bc, bs, n, k, layout, desc, rdesc, yc, ys, out_layout,
-                                             _raw_stream(dev)), "mxfp4_gemm_epilogue_requant")
+                                             _stream(dev)), "mxfp4_gemm_epilogue_requant")
     return y_codes, y_scales
 
 
@@ -375,7 +386,7 @@ def gemm_glu(a_codes, a_scales, g_codes, g_scales, u_codes, u_scales, act="silu"
     ac, as_ = _packed("operand A", a_codes, a_scales, m, k, layout, dev)
     desc = _glu_desc(act, g_codes, g_scales, u_codes, u_scales, bias_g, bias_u, n, k, layout, dev)
     y, ptr, ld, yt = _dense_output(y, m, n, out_dtype, a_codes)
-    _check(lib().mxfp4_gemm_glu(ac, as_, m, desc, n, k, layout, ptr, yt, ld, _raw_stream(dev)), "mxfp4_gemm_glu")
+    _check(lib().mxfp4_gemm_glu(ac, as_, m, desc, n, k, layout, ptr, yt, ld, _stream(dev)), "mxfp4_gemm_glu")
     return y
 
 
@@ -389,7 +400,7 @@ def gemm_glu_requant(a_codes, a_scales, g_codes, g_scales, u_codes, u_scales, ac
     desc = _glu_desc(act, g_codes, g_scales, u_codes, u_scales, bias_g, bias_u, n, k, layout, dev)
     rdesc, _keep = _rotation(rot, a_codes, n)
     y_codes, y_scales, yc, ys = _packed_outputs(m, n, out_layout, y_codes, y_scales, a_codes)
-    _check(lib().mxfp4_gemm_glu_requant(ac, as_, m, desc, n, k, layout, rdesc, yc, ys, out_layout, _raw_stream(dev)),
+    _check(lib().mxfp4_gemm_glu_requant(ac, as_, m, desc, n, k, layout, rdesc, yc, ys, out_layout, _stream(dev)),
            "mxfp4_gemm_glu_requant")
     return y_codes, y_scales
 
@@ -436,7 +447,7 @@ def ffn(x, p: Norm, residual, w_up, w_down, hidden: int, w_gate=None, act="silu"
     work = torch.empty(total, dtype=torch.uint8, device=x.device)
     base = work.data_ptr()
     xc, xs, hc, hs = (base + at for at in starts)
-    L, stream = lib(), _raw_stream(dev)
+    L, stream = lib(), _stream(dev)
     _check(L.mxfp4_norm_quantize(desc, rdesc, layout, xc, xs, stream), "mxfp4_norm_quantize")
     if w_gate is not None:
         _check(L.mxfp4_gemm_glu_requant(xc, xs, rows, glu, hidden, d, layout, rdesc, hc, hs, layout, stream),
