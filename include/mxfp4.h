@@ -409,6 +409,8 @@ MXFP4_API mxfp4_status mxfp4_norm(const mxfp4_norm_args* a, void* y, int32_t y_d
  *   rot     NULL / NONE, HADAMARD32, SMOOTH or KRON.
  *   layout, codes, scales  as for mxfp4_quantize_rotate (TILED: the padding
  *           rows are not written).
+ * With KRON and past some 10000 rows the two calls are faster (57344 x 3072: 209
+ * against 238 us); with the other rotations this one is (H32 129 against 192).
  * Errors: as mxfp4_norm (y aside), INVALID_ARG for null codes or scales,
  *   d % 32 != 0 (d % 128 for TILED), a bad layout or rotation; UNSUPPORTED for
  *   pointers or row strides that are not 16-byte aligned (TILED scales: 4),
@@ -436,6 +438,10 @@ typedef struct {
 
 /* mxfp4_gemm with an epilogue (NULL: none).  Operands, sizes and Y as for
  * mxfp4_gemm; bias, gate and residual need the alignment of their elements.
+ * The bias is added to the finished sum, in one rounding.
+ * ROWMAJOR with k % 128 != 0 and more than 64 rows streams the weights once
+ * for every 64 rows: past 500 to 1000 rows mxfp4_gemm and separate elementwise
+ * kernels are faster (2048 x 2880 -> 2880 with GELU: 68 against 109 us).
  * Errors: as mxfp4_gemm; INVALID_ARG for a bad activation or dtype, ld_gate or
  *   ld_res below n, group_rows < 1 with a gate, reserved != 0; UNSUPPORTED for
  *   pointers not aligned to their elements, or sizes past the grid

@@ -32,11 +32,12 @@
 // Bound by the matrix pipe at the clock the power limit leaves, then by the
 // epilogue, during which a CU's only 256 x 256 tile feeds no MFMA.  Measured
 // (bf16, H32 where MXFP4; the GEMM without an epilogue in brackets):
-//  * 57344 x 3072 -> 12288, bias, tanh GELU   1147-1263 us, 3.4-3.8 PF/s (1018)
-//  * 8192 x 4096 -> 2 x 14336, gated silu      441-477 us, 4.0-4.4 PF/s (434)
-//  * 3584 x 12288 -> 3072, bias, gate, residual 78-83 us, 3.3-3.5 PF/s (69.5)
-//  * 3584 x 3072 -> 12288, tanh GELU, H32, MXFP4  95 us, 2.8 PF/s (72.6)
-//  * 523 x 1408 -> 2 x 3001 fp32, gated, bias      12 us (128 x 128 tiles)
+//  * 57344 x 3072 -> 12288, bias, tanh GELU   1171-1278 us, 3.4-3.7 PF/s (1018)
+//  * 8192 x 4096 -> 2 x 14336, gated silu      455-477 us, 4.0-4.2 PF/s (434)
+//  * 3584 x 12288 -> 3072, bias, gate, residual 79-84 us, 3.2-3.4 PF/s (69.5)
+//  * 3584 x 3072 -> 12288, tanh GELU, H32, MXFP4  91-100 us, 2.7-3.0 PF/s (72.6)
+//  * 523 x 1408 -> 2 x 3001 fp32, gated, bias      12-13 us (128 x 128 tiles)
+// (over the cards; within a card to 1%.)
 #pragma once
 #include "gemm_large_core.h"
 #include "activation.h"

@@ -6,14 +6,13 @@
 //
 // Bound by HBM: x and the residual are read once, r and y (or 4.25 bits an
 // element of y) written once (57344 x 3072, layer norm with gate and modulation:
-// 1.41 GB in 243 us, 5.8 TB/s; a large copy reaches 5.1-5.4).  A workgroup of 1
+// 1.41 GB in 244 us, 5.8 TB/s; a large copy reaches 5.1-5.5).  A workgroup of 1
 // to 16 waves owns a row; every lane keeps its columns of the row in registers
 // as chunks of 8 consecutive elements (16 bytes of bf16: a wave's load
 // instruction covers 1 KiB of the row), so the statistics, which need the whole
 // row, cost no second read.  Statistics are fp32: per-lane sums, then the wave's
-// sum by lane permutes, then (several waves) one
-// LDS exchange; the layer norm's variance is the mean square of the centred
-// values, not a difference of moments.
+// sum by lane permutes, then (several waves) one LDS exchange; the layer norm's
+// variance is the mean square of the centred values, not a difference of moments.
 //
 // MXFP4 result: a 32-element block is four neighbouring lanes (a quad), so the
 // block amax and the Hadamard's strides 8 and 16 are quad permutes and a lane
