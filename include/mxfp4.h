@@ -492,6 +492,156 @@ MXFP4_API mxfp4_status mxfp4_gemm_glu_requant(const uint8_t* a_codes, const uint
                                               const mxfp4_rotation* rot, uint8_t* y_codes, uint8_t* y_scales,
                                               int32_t y_layout, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Mixture of experts: the feed-forward block of a model whose MLP is split over
+ * experts.  Each token goes through topk of them, and their results are added
+ * with the router's weights:
+ *   mxfp4_moe_route   the experts and weights of each token, from router logits
+ *   mxfp4_moe_plan    the (token, choice) pairs in expert order
+ *   mxfp4_moe_up      H = act(A G_e^T + bias_g) * (A U_e^T + bias_u), or
+ *                     act(A U_e^T + bias_u), for every pair (..._requant: MXFP4)
+ *   mxfp4_moe_down    y = residual + sum over a token's choices of
+ *                     weight * (h D_e^T + bias)
+ * A pair's number is token * topk + choice; its row in H is plan.slot[pair].
+ * Sizes: 1 <= topk <= 64, 1 <= experts <= 1024, tokens * topk < 2^28, else
+ * MXFP4_ERR_UNSUPPORTED (INVALID_ARG below 1).  The same inputs give the same
+ * bits on every run: no sum depends on the order in which workgroups finish. */
+
+typedef enum {
+    MXFP4_SCORE_SOFTMAX = 0,
+    MXFP4_SCORE_SIGMOID = 1
+} mxfp4_score;
+
+/* Score of a group of experts: its largest key, or the sum of its two largest
+ * (of one where only one can be chosen). */
+typedef enum {
+    MXFP4_GROUP_MAX = 0,
+    MXFP4_GROUP_TOP2 = 1
+} mxfp4_group_score;
+
+/* Router.  Scores s = softmax(logits) or sigmoid(logits) over a token's experts.
+ * Experts are chosen by their keys: the logits, or s + bias where there is a
+ * bias (which is in the choice only, not in the weights).  With groups > 1 the
+ * experts are that many consecutive groups of equal size; the topk_groups best by
+ * group score (of s + bias, or of s without a bias) are kept, the others left
+ * out.  Then the topk largest keys, in descending order, ties to the lowest
+ * index, between groups too.  weights = s of the chosen, divided by their sum if
+ * renormalize (0 where that sum is 0), times scale.  Scores, keys with a bias and
+ * group scores are formed in binary64, weights rounded once.
+ * Logits of -infinity or NaN are experts that cannot be chosen; a bias of
+ * -infinity takes one out as well.  Where fewer than topk can be chosen, the
+ * remaining ids are -1 with weight 0. */
+typedef struct {
+    int32_t score;         /* mxfp4_score */
+    int32_t topk;          /* 1 .. experts */
+    int32_t groups;        /* 1 .. 64, divides experts */
+    int32_t topk_groups;   /* 1 .. groups */
+    int32_t group_score;   /* mxfp4_group_score */
+    int32_t renormalize;
+    float scale;           /* finite */
+    int32_t reserved;      /* must be 0 */
+    const float* bias;     /* device [experts], or NULL */
+} mxfp4_router;
+
+/*   logits  device [tokens][ld] of dtype, ld >= experts
+ *   ids     device [tokens][topk] (written);  weights  the same
+ * Errors: INVALID_ARG for null pointers (when tokens > 0), bad enums, sizes out
+ *   of their ranges, a scale that is not finite; UNSUPPORTED for pointers not
+ *   aligned to their elements, tokens >= 2^30, groups > 64, and the limits
+ *   above; HIP if the launch fails. */
+MXFP4_API mxfp4_status mxfp4_moe_route(const void* logits, int32_t dtype, int64_t tokens, int64_t experts,
+                                       int64_t ld, const mxfp4_router* r, int32_t* ids, float* weights,
+                                       void* stream);
+
+/* Plan: the pairs whose expert is first .. first + experts - 1 (a GPU that holds
+ * a part of the experts passes its own), sorted by expert and within one by
+ * number.  Other ids (-1 among them) belong to no expert here: such pairs have no
+ * row and add nothing to their token.  The same expert may be given twice to a
+ * token; it then counts twice.
+ * The plan is int32 words in device memory, 16-byte aligned, of
+ * mxfp4_moe_plan_bytes bytes.  The first are its result:
+ *   offsets [experts + 1]     first row of each expert, and the number of rows
+ *   order   [tokens * topk]   pair of each row; -1 behind the last row
+ *   slot    [tokens * topk]   row of each pair; -1 where it has none
+ * The rest is for the products, which take the plan with the sizes it was made
+ * with.  A plan needs no clearing and may be written again.
+ * Errors: INVALID_ARG for negative sizes, first < 0, null pointers, too few
+ *   bytes; UNSUPPORTED for misaligned pointers, first >= 2^30, and the limits
+ *   above; HIP if a launch fails. */
+MXFP4_API mxfp4_status mxfp4_moe_plan_bytes(int64_t tokens, int64_t topk, int64_t experts, int64_t* bytes);
+MXFP4_API mxfp4_status mxfp4_moe_plan(const int32_t* ids, int64_t tokens, int64_t topk, int64_t first,
+                                      int64_t experts, void* plan, int64_t plan_bytes, void* stream);
+
+/* The experts' up projections.  Weights are stacks: expert e's codes and scales
+ * follow expert e - 1's, each expert's as mxfp4_quantize_rotate leaves n rows of k
+ * in `layout` (TILED: each padded to whole tiles). */
+typedef struct {
+    int32_t act;              /* mxfp4_act */
+    int32_t vec_dtype;        /* mxfp4_dtype of the biases */
+    const uint8_t* u_codes;   /* up projections */
+    const uint8_t* u_scales;
+    const uint8_t* g_codes;   /* gate projections, or NULL: not gated */
+    const uint8_t* g_scales;
+    const void* bias_u;       /* device [experts][n], or NULL */
+    const void* bias_g;       /* device [experts][n], or NULL */
+    int32_t reserved;         /* must be 0 */
+} mxfp4_moe_up_weights;
+
+/*   a_codes/a_scales  the tokens' activations, [tokens] rows of k in `layout`
+ *   plan              of (tokens, topk, experts)
+ *   y                 device, row p for row p of the plan: [tokens * topk][ld_y];
+ *                     rows behind the plan's last are left as they are
+ * Errors: INVALID_ARG as mxfp4_gemm_glu, for a null plan, and for a gate's
+ *   scales or bias without its codes; UNSUPPORTED for misaligned pointers (codes
+ *   and plan 16 bytes, scales 4 where k is a multiple of 128, biases and y their
+ *   elements), n or k >= 2^30, code bytes of A or of one expert past 2^32, and
+ *   the limits above; HIP if the launch fails. */
+MXFP4_API mxfp4_status mxfp4_moe_up(const uint8_t* a_codes, const uint8_t* a_scales, const void* plan,
+                                    int64_t tokens, int64_t topk, int64_t experts,
+                                    const mxfp4_moe_up_weights* w, int64_t n, int64_t k, int32_t layout, void* y,
+                                    int32_t y_dtype, int64_t ld_y, void* stream);
+
+/* The same with an MXFP4 result of tokens * topk rows (rows behind the plan's
+ * last are not written): the bytes that mxfp4_quantize_rotate with `rot` gives for
+ * mxfp4_moe_up's fp32 y.  rot, y_codes, y_scales, y_layout and their errors as for
+ * mxfp4_gemm_glu_requant. */
+MXFP4_API mxfp4_status mxfp4_moe_up_requant(const uint8_t* a_codes, const uint8_t* a_scales, const void* plan,
+                                            int64_t tokens, int64_t topk, int64_t experts,
+                                            const mxfp4_moe_up_weights* w, int64_t n, int64_t k, int32_t layout,
+                                            const mxfp4_rotation* rot, uint8_t* y_codes, uint8_t* y_scales,
+                                            int32_t y_layout, void* stream);
+
+/* The experts' down projections and the sum over a token's choices. */
+typedef struct {
+    const uint8_t* codes;     /* stacks, as above: n rows of k for each expert */
+    const uint8_t* scales;
+    const void* bias;         /* device [experts][n] of vec_dtype, or NULL */
+    int32_t vec_dtype;
+    int32_t reserved;         /* must be 0 */
+} mxfp4_moe_down_weights;
+
+/*   h_codes/h_scales  [tokens * topk] rows of k in `layout`, in the plan's order
+ *   weights           device [tokens][topk] fp32 (not read for pairs without a row)
+ *   residual          device [tokens][ld_res] of res_dtype, or NULL; may be y
+ *                     itself with its type and stride
+ *   y                 device [tokens][ld_y] of y_dtype.  Sums in fp32, in the order
+ *                     of a token's choices, the residual first.  For a bf16 y the
+ *                     single products may be held in 16 bits, 11 of them
+ *                     significant: an eighth of bf16's rounding
+ *   workspace         device, 256-byte aligned, of mxfp4_moe_down_workspace bytes
+ *                     (the products); needs no clearing, and calls that may
+ *                     overlap in time need one each
+ * Errors: as mxfp4_moe_up (a null weights or workspace, or a short one, is
+ *   INVALID_ARG). */
+MXFP4_API mxfp4_status mxfp4_moe_down_workspace(int64_t tokens, int64_t topk, int64_t experts, int64_t n, int64_t k,
+                                                int32_t layout, int32_t y_dtype, int64_t* bytes);
+MXFP4_API mxfp4_status mxfp4_moe_down(const uint8_t* h_codes, const uint8_t* h_scales, const void* plan,
+                                      int64_t tokens, int64_t topk, int64_t experts, const float* weights,
+                                      const mxfp4_moe_down_weights* w, int64_t n, int64_t k, int32_t layout,
+                                      const void* residual, int32_t res_dtype, int64_t ld_res, void* y,
+                                      int32_t y_dtype, int64_t ld_y, void* workspace, int64_t workspace_bytes,
+                                      void* stream);
+
 /* Static description of a status code (never NULL). */
 MXFP4_API const char* mxfp4_status_string(int32_t status);
 

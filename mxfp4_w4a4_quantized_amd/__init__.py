@@ -14,6 +14,8 @@ C-ABI calls declared in include/mxfp4.h:
   inverse_transpose(m)               host helper for the Kronecker weight fold
   norm, norm_quantize, gemm_epilogue, gemm_epilogue_requant, gemm_glu,
   gemm_glu_requant, ffn              the feed-forward operators (feedforward.py)
+  moe_route, moe_plan, moe_up, moe_up_requant, moe_down, moe_ffn
+                                     the mixture-of-experts operators (moe.py)
 
 Layouts: ROWMAJOR (codes [rows, k/2], scales [rows, k/32]) or TILED, the
 GEMM-native layout of include/mxfp4.h (256-row tiles x 128-element stages,
@@ -52,7 +54,9 @@ EXPORTED = ("mxfp4_quantize_rotate", "mxfp4_quantize_fit", "mxfp4_gemm", "mxfp4_
             "mxfp4_tiled_bytes",
             "mxfp4_inverse_transpose", "mxfp4_smooth_weight_factors", "mxfp4_status_string",
             "mxfp4_abi_version", "mxfp4_norm", "mxfp4_norm_quantize", "mxfp4_gemm_epilogue",
-            "mxfp4_gemm_epilogue_requant", "mxfp4_gemm_glu", "mxfp4_gemm_glu_requant")
+            "mxfp4_gemm_epilogue_requant", "mxfp4_gemm_glu", "mxfp4_gemm_glu_requant", "mxfp4_moe_route",
+            "mxfp4_moe_plan_bytes", "mxfp4_moe_plan", "mxfp4_moe_up", "mxfp4_moe_up_requant",
+            "mxfp4_moe_down_workspace", "mxfp4_moe_down")
 LINEAR_SMALL_MAX_M = 64
 
 
@@ -106,8 +110,9 @@ def lib() -> ctypes.CDLL:
     L.mxfp4_status_string.argtypes = [i32]
     L.mxfp4_abi_version.restype = i32
     L.mxfp4_abi_version.argtypes = []
-    from .feedforward import declare
-    declare(L)
+    from . import feedforward, moe
+    feedforward.declare(L)
+    moe.declare(L)
     _lib = L
     return L
 
@@ -497,3 +502,5 @@ def inverse_transpose(m: np.ndarray) -> np.ndarray:
 
 from .feedforward import (Epilogue, Norm, ffn, gemm_epilogue, gemm_epilogue_requant,  # noqa: E402,F401
                           gemm_glu, gemm_glu_requant, norm, norm_quantize)
+from .moe import (ExpertPlan, Router, moe_down, moe_down_workspace, moe_ffn, moe_plan, moe_route,  # noqa: E402,F401
+                  moe_up, moe_up_requant, quantize_experts)

@@ -21,7 +21,8 @@ LIB = os.path.join(HERE, "libmxfp4.so")
 CEILING_LIB = os.path.join(HERE, "libmxfp4_ceiling.so")
 SOURCES = ["api.cpp", "api_ffn.cpp", "quantize.hip", "gemm.hip", "gemm_large.hip", "gemm_small.hip",
            "gemm_fused_small.hip", "gemm_fused_large.hip", "gemm_glu_large.hip",
-           "gemm_residual_large.hip", "norm.hip"]
+           "gemm_residual_large.hip", "norm.hip", "api_moe.cpp", "moe_route.hip", "moe_small.hip",
+           "moe_tiles.hip", "moe_glu_tiles.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

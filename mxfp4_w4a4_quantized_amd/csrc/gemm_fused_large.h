@@ -41,7 +41,9 @@
 #pragma once
 #include "gemm_large_core.h"
 #include "activation.h"
+#include "moe_tile.h"
 
+#include <type_traits>
 #include <utility>
 
 namespace mxfp4 {
@@ -174,13 +176,36 @@ __device__ __forceinline__ void hadamard_fragment(float (&v)[16]) {
   for (int i = 0; i < 16; i += 2) swap_halves(v[i], v[i + 1]);
 }
 
+// Two fp32 -> packed 16-bit floats (low half = a), round to nearest even.
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, f16x2));
+}
+
+// Workgroups that a number of tiles is spread over, of `most`: the fewest (a
+// multiple of 8) that need no more rounds, as large_grid does on the host.
+__device__ __forceinline__ int balanced_grid(int ntiles, int most) {
+  if (ntiles <= most) return ntiles;
+  const int rounds = (ntiles + most - 1) / most;
+  return min(most, ((ntiles + rounds - 1) / rounds + 7) / 8 * 8);
+}
+
 // ACT: A_LINEAR or an mxfp4_act.  OUT: 0 fp32, 1 bf16, 2 MXFP4.  RES: 0 no gate
 // or residual; 1 / 2 a gate and/or a residual (bf16 / fp32) in whole aligned
 // pieces of 4 columns, with at most two gate rows per wave; 3 any other.
-template <class T, int ACT, int OUT, int RES, bool GLU>
-__global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(FusedArgs f, int tiles_m, int tiles_n, int grid,
+//
+// Args MoeArgs: the experts' products.  The tiles are those of the plan's row
+// tiles, an expert's in one run (so that they share its weights in L2); how many
+// there are is read from the plan, and workgroups without one leave.  A tile's
+// weights are its expert's, its activation rows go by the plan's token numbers,
+// a lane's 16 bytes of a row wherever the row lies.  OUT 3: 16-bit floats with a
+// power of two per row and 32 columns.
+template <class T, int ACT, int OUT, int RES, bool GLU, class Args = FusedArgs>
+__global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(Args f, int tiles_m, int tiles_n, int grid,
                                                                  int xcd_remap) {
+  constexpr bool MOE = std::is_same<Args, MoeArgs>::value;
   static_assert(RES == 0 || (OUT != 2 && !GLU), "gate and residual are for plain dense outputs");
+  static_assert(!MOE || RES == 0, "no gate or residual in the experts' products");
   constexpr int BN = T::BN, BM = T::BM, NBUF = T::NBUF, WN = T::WN, WM = T::WM, NW = T::NW, FN = T::FN, FM = T::FM;
   constexpr int CODE_BYTES = T::CODE_BYTES, STAGE_BYTES = T::STAGE_BYTES, LPS = T::LPS, NRD = T::NRD;
   constexpr int CODE_LOADS = T::CODE_LOADS, SCALE_LOADS = T::SCALE_LOADS, CODE_LOADS_B = T::CODE_LOADS_B;
@@ -190,6 +215,13 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(FusedAr
   __shared__ __attribute__((aligned(1024))) uint8_t lds[NBUF * STAGE_BYTES + (PIECES && FM * FN == 4 ? 1024 : 0)];
 
   const GemmArgs& g = f.g;
+  constexpr int HI = moe::height_index(BM);
+  if constexpr (MOE) {
+    tiles_m = moe::uniform(f.ntiles + HI);
+    grid = __builtin_amdgcn_readfirstlane(balanced_grid(tiles_m * tiles_n, grid));
+    xcd_remap = (grid % 8) == 0;
+    if ((int)blockIdx.x >= grid) return;
+  }
   const int ntiles = tiles_m * tiles_n;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -227,28 +259,61 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(FusedAr
   constexpr int NCB = !T::WHOLE ? CODE_LOADS : GLU ? 2 : 1;
   auto cb = [](int i) { return NCB == CODE_LOADS ? i : NCB == 2 ? (i >> 1) & 1 : 0; };
   const uint8_t *cbase[NCB], *sbase[SCALE_LOADS];
+  auto bases = [&](int64_t dc, int64_t ds) __attribute__((always_inline)) {   // dc, ds: the weights' distance from the first expert's
 #pragma unroll
-  for (int i = 0; i < NCB; ++i) {
-    const int q = NCB == 2 ? 2 * i : code_group(i);   // (a wave's load count is a multiple of 4)
-    cbase[i] = reinterpret_cast<const uint8_t*>(!code_w(i) ? +pa : (q & 2) ? +pu : +pb);
-  }
+    for (int i = 0; i < NCB; ++i) {
+      const int q = NCB == 2 ? 2 * i : code_group(i);   // (a wave's load count is a multiple of 4)
+      cbase[i] = reinterpret_cast<const uint8_t*>(!code_w(i) ? +pa : (q & 2) ? pu + dc : pb + dc);
+    }
 #pragma unroll
-  for (int i = 0; i < SCALE_LOADS; ++i)
-    sbase[i] = reinterpret_cast<const uint8_t*>(!scale_w(i) ? +qa : lane >= 32 ? +qu : +qb);
+    for (int i = 0; i < SCALE_LOADS; ++i)
+      sbase[i] = reinterpret_cast<const uint8_t*>(!scale_w(i) ? +qa : lane >= 32 ? qu + ds : qb + ds);
+  };
+  if constexpr (!MOE) bases(0, 0);
+  // The j-th tile of this workgroup: its first activation row, the end of its
+  // rows, its place along N and (MOE) its expert.
+  struct Place { int row0, end, tn, expert; };
+  auto place = [&](int j) __attribute__((always_inline)) {
+    Place p;
+    int tm;
+    if constexpr (MOE) {
+      const int L = j * grid + slot, rt = __builtin_amdgcn_readfirstlane(L / tiles_n);
+      const moe::i32x4 e = moe::uniform4(f.tiles[HI] + 4 * (int64_t)rt);
+      tile_coords(L - e[3] * tiles_n, (e[2] - e[1] + BM - 1) / BM, tiles_n, tm, p.tn);
+      p.row0 = __builtin_amdgcn_readfirstlane(e[1] + tm * BM);
+      p.tn = __builtin_amdgcn_readfirstlane(p.tn);
+      p.end = e[2];
+      p.expert = e[0];
+    } else {
+      tile_coords(j * grid + slot, tiles_m, tiles_n, tm, p.tn);
+      p.row0 = tm * BM;
+      p.end = g.m;
+      p.expert = 0;
+    }
+    return p;
+  };
   uint32_t coff[CODE_LOADS], soff[SCALE_LOADS];
-  auto plan = [&](int j) {   // j-th tile of this workgroup
-    int tm, tn;
-    tile_coords(j * grid + slot, tiles_m, tiles_n, tm, tn);
+  auto plan = [&](int j) __attribute__((always_inline)) {
+    const Place at = place(j);
+    const int tn = at.tn;
+    if constexpr (MOE) bases(at.expert * f.w_codes, at.expert * f.w_scales);
 #pragma unroll
     for (int i = 0; i < CODE_LOADS; ++i) {
       const int q = code_group(i);
       const bool w = code_w(i);
-      const int row0 = w ? tn * TN + (GLU ? 32 * (q >> 2) + 16 * (q & 1) : 16 * q) : tm * BM + 16 * q - BN;
-      if (tiled) {
+      const int row0 = w ? tn * TN + (GLU ? 32 * (q >> 2) + 16 * (q & 1) : 16 * q) : at.row0 + 16 * q - BN;
+      if (MOE && !w) {
+        // (a tile's row r lies in a swizzle of its own: the source's is undone)
+        const int in = 16 * q - BN + (lane >> 2);
+        const uint32_t src = (uint32_t)moe::source_row(f, min(at.row0 + in, at.end - 1));
+        const uint32_t chunk = (uint32_t)((lane & 3) ^ swz(in & 255));
+        coff[i] = tiled ? (src >> 8) * nstage * (16 * 1024) + (src & 255) * 64 + 16 * (chunk ^ (uint32_t)swz((int)(src & 255)))
+                        : src * kbytes + 16 * chunk;
+      } else if (tiled) {
         coff[i] = (uint32_t)(row0 >> 8) * nstage * (16 * 1024) + (uint32_t)(row0 & 255) * 64 + lane * 16;
       } else {
         const int row = row0 + (lane >> 2);
-        const uint32_t grow = (uint32_t)min(row, (w ? g.n : g.m) - 1);
+        const uint32_t grow = (uint32_t)min(row, (w ? g.n : at.end) - 1);
         coff[i] = grow * kbytes + 16u * (uint32_t)((lane & 3) ^ swz(row & 255));
       }
     }
@@ -256,27 +321,28 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(FusedAr
     for (int i = 0; i < SCALE_LOADS; ++i) {
       const int q = scale_group(i);
       const bool w = scale_w(i);
-      const int row = w ? tn * TN + (GLU ? 32 * q + lr : 64 * q + lane) : tm * BM + 64 * q - BN + lane;
+      int row = w ? tn * TN + (GLU ? 32 * q + lr : 64 * q + lane) : at.row0 + 64 * q - BN + lane;
+      if (MOE && !w) row = moe::source_row(f, min(row, at.end - 1));
       soff[i] = tiled ? (uint32_t)(row >> 8) * nstage * 1024 + (uint32_t)(row & 255) * 4
-                      : (uint32_t)min(row, (w ? g.n : g.m) - 1) * kblocks;
+                      : (uint32_t)(MOE && !w ? row : min(row, (w ? g.n : at.end) - 1)) * kblocks;
     }
   };
   const uint32_t cstride = tiled ? 16 * 1024 : RB, sstride = tiled ? 1024 : 4;   // bytes per stage
   int ij = 0, ikt = 0, ibuf = 0;   // issue state: tile, stage within it, ring slot
   plan(0);
-  auto issue_codes = [&](int i0, int i1) {
+  auto issue_codes = [&](int i0, int i1) __attribute__((always_inline)) {
     uint8_t* dst = lds + ibuf * STAGE_BYTES;
 #pragma unroll
     for (int i = i0; i < i1; ++i)
       load_lds16(cbase[cb(i)] + ikt * cstride + coff[i], dst + code_group(i) * 1024);
   };
-  auto issue_scales = [&]() {
+  auto issue_scales = [&]() __attribute__((always_inline)) {
     uint8_t* dst = lds + ibuf * STAGE_BYTES + CODE_BYTES;
 #pragma unroll
     for (int i = 0; i < SCALE_LOADS; ++i)
       load_lds4(sbase[i] + ikt * sstride + soff[i], dst + 256 * scale_group(i));
   };
-  auto advance = [&]() {
+  auto advance = [&]() __attribute__((always_inline)) {
     ibuf = ibuf + 1 == NBUF ? 0 : ibuf + 1;
     if (++ikt == nk) {
       ikt = 0;
@@ -316,23 +382,22 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(FusedAr
   asm volatile("" : "+v"(zero));
   const bool biased = f.bias != nullptr || (GLU && f.bias_u != nullptr);
   float bias[FN];
-  auto load_bias = [&](int tn) {
+  auto load_bias = [&](int tn, int expert) {
 #pragma unroll
     for (int a = 0; a < FN; ++a) {
       const void* src = GLU && (a & 1) ? f.bias_u : f.bias;
       const int n = tn * TN + wn * WCOLS + 32 * (GLU ? a >> 1 : a) + lr;
       bias[a] = 0.0f;
-      if (src != nullptr && lg == 0 && n < g.n) bias[a] = vec_elem(src, f.vec_bf16, n);
+      if (src != nullptr && lg == 0 && n < g.n) bias[a] = vec_elem(src, f.vec_bf16, MOE ? (int64_t)expert * g.n + n : n);
     }
   };
 
   // The ring always has NBUF - 1 stages in flight (see gemm_large_kernel).
-#pragma unroll
-  for (int p = 0; p < NBUF - 1; ++p) {
-    if (p > 0) advance();
+  each([&](auto p) __attribute__((always_inline)) {
+    if constexpr (p > 0) advance();
     issue_codes(0, CODE_LOADS);
     issue_scales();
-  }
+  }, std::make_integer_sequence<int, NBUF - 1>{});
   v16f acc[FN][FM];
 #pragma unroll
   for (int a = 0; a < FN; ++a)
@@ -354,9 +419,9 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(FusedAr
   // against 425 us with it).
   constexpr bool AHEAD = PIECES && FM * FN == 4;
   constexpr int PF = 8;
-  auto prefetch_res = [&](int tm, int tn) {
+  auto prefetch_res = [&](int row0, int tn) {
     constexpr int RSZ = RES == 1 ? 2 : 4, LINES = WCOLS * RSZ / 128;   // per row
-    const int mw0 = tm * BM + wm * (BM / WM), nw0 = tn * TN + wn * WCOLS;
+    const int mw0 = row0 + wm * (BM / WM), nw0 = tn * TN + wn * WCOLS;
     const uint8_t* res = static_cast<const uint8_t*>(f.residual);
 #pragma unroll
     for (int i = 0; i < BM / WM * LINES / 64; ++i) {
@@ -368,17 +433,17 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(FusedAr
 
   int cbuf = 0;   // ring slot of the stage being computed
   for (int j = 0; j * nk < total; ++j) {
-    int tm, tn;
-    tile_coords(j * grid + slot, tiles_m, tiles_n, tm, tn);
+    const Place at = place(j);
+    const int tn = at.tn, end = at.end;
     const int ahead = AHEAD && f.residual != nullptr ? max(nk - PF, 0) : nk;
-    if (biased) load_bias(tn);
+    if (biased) load_bias(tn, at.expert);
     // the compiler does not see the accumulators being cleared (inline asm):
     // wait states before the K loop's MFMAs read them
     mfma_wait();
 
     for (int kt = 0; kt < nk; ++kt) {
       if constexpr (AHEAD) {
-        if (kt == ahead) prefetch_res(tm, tn);
+        if (kt == ahead) prefetch_res(at.row0, tn);
       }
       advance();   // to stage it + NBUF - 1
       wait_stages<NBUF - 3, LPS>();
@@ -416,7 +481,7 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(FusedAr
     }
 
     // ---- epilogue of this workgroup's j-th tile
-    const int mw0 = tm * BM + wm * (BM / WM), nw0 = tn * TN + wn * WCOLS;   // the wave's block of Y
+    const int mw0 = at.row0 + wm * (BM / WM), nw0 = tn * TN + wn * WCOLS;   // the wave's block of Y
     const bool relu = f.act == act::RELU;
     constexpr int NO = GLU ? FN / 2 : FN;   // output fragments along N
 
@@ -484,7 +549,7 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(FusedAr
           crow = g.q_codes + (int64_t)m * (g.n >> 1) + (nw0 >> 1);
           srow = g.q_scales + (int64_t)m * (g.n >> 5) + (nw0 >> 5);
         }
-        const bool row_ok = m < g.m;
+        const bool row_ok = m < end;
 #pragma unroll
         for (int o = 0; o < NO; ++o) {
           float v[16];
@@ -527,14 +592,14 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(FusedAr
       // c ^ (r % chunks), which spreads both the writes (32 rows, one chunk)
       // and the reads (whole rows) over the banks.  SE: bytes of a staged
       // element (bf16 only where nothing is added after it).
-      constexpr int SE = OUT == 1 && RES == 0 ? 2 : 4;
+      constexpr int SE = (OUT == 1 || OUT == 3) && RES == 0 ? 2 : 4;
       // fragments per pass: whole 256-byte rows where the ring slot holds them
       constexpr int MAXF = (STAGE_BYTES / (NW * 32) >= 256 ? 256 : 128) / (32 * SE);
       constexpr int FPP = NO < MAXF ? NO : MAXF;
       constexpr int SB = FPP * 32 * SE;
       constexpr int LPR = SB / 16, RPI = 64 / LPR;          // lanes (chunks) per row, rows per instruction
       constexpr int EPL = 16 / SE;                          // elements per lane
-      constexpr int OSZ = OUT == 1 ? 2 : 4;                 // bytes of an output element
+      constexpr int OSZ = OUT == 1 || OUT == 3 ? 2 : 4;     // bytes of an output element
       static_assert(NW * 32 * SB <= STAGE_BYTES, "staging area");
       const int lslot = cbuf == 0 ? NBUF - 1 : cbuf - 1;
       uint8_t* tb = lds + lslot * STAGE_BYTES + wave * (32 * SB);
@@ -599,7 +664,7 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(FusedAr
       }
       // RES 0: whole aligned pieces, and nothing to leave out of the tile
       const bool vec = ((uintptr_t)g.y % 16) == 0 && ((g.ld_y * OSZ) % 16) == 0;
-      const bool full = vec && (tm + 1) * BM <= g.m && (tn + 1) * TN <= g.n;
+      const bool full = vec && at.row0 + BM <= end && (tn + 1) * TN <= g.n;
       __builtin_amdgcn_s_barrier();   // every wave is done reading that slot
       each([&](auto pass) __attribute__((always_inline)) {
         constexpr int p = pass;
@@ -612,11 +677,31 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(FusedAr
         for (int o = o0; o < o0 + FPP; ++o) {
           float v[16];
           take(o, bb, v);
+          if constexpr (OUT == 3) {
+            // 2^14 <= amax < 2^15 after scaling: no overflow, and 11 bits for every
+            // value down to 2^-29 of the block's largest (the exponent stays in 1 .. 254)
+            float am = 0.0f;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) am = fmaxf(am, fabsf(v[r]));
+            float other = am;
+            swap_halves(am, other);
+            am = fmaxf(am, other);
+            const uint32_t ef = min(max(__float_as_uint(am) >> 23, 15u), 254u);   // of 2^(ef - 127)
+            const float sc = __uint_as_float((268u - ef) << 23);                   // 2^(14 - (ef - 127))
+#pragma unroll
+            for (int r = 0; r < 16; ++r) v[r] = v[r] * sc;
+            const int m = mw0 + 32 * bb + lr, n = nw0 + 32 * o;
+            if (lg == 0 && m < end && n < g.n)
+              f.z_scales[(int64_t)m * (g.n >> 5) + (n >> 5)] = (uint8_t)(ef - 14u);
+          }
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
             const int at = ((o - o0) * 32 + 8 * t + 4 * lg) * SE;
             uint8_t* dst = tb + lr * SB + (((at >> 4) ^ (lr & (LPR - 1))) << 4) + (at & 15);
-            if constexpr (SE == 2) {
+            if constexpr (OUT == 3) {
+              *reinterpret_cast<uint2*>(dst) =
+                  make_uint2(pack_f16(v[4 * t], v[4 * t + 1]), pack_f16(v[4 * t + 2], v[4 * t + 3]));
+            } else if constexpr (SE == 2) {
               *reinterpret_cast<uint2*>(dst) =
                   make_uint2(pack_bf16(v[4 * t], v[4 * t + 1]), pack_bf16(v[4 * t + 2], v[4 * t + 3]));
             } else {
@@ -642,7 +727,7 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(FusedAr
             for (int r = 0; r < 32 / RPI; ++r) {
               const u32x4 v = staged(r);
               uint8_t* yp = y0 + (int64_t)r * RPI * g.ld_y * OSZ;
-              if (m0 + RPI * r >= g.m) continue;
+              if (m0 + RPI * r >= end) continue;
               if (vec && n0 + EPL <= g.n) {
                 *reinterpret_cast<u32x4*>(yp) = v;
               } else {

@@ -127,6 +127,21 @@ hipError_t launch_fused_tiles(const FusedArgs& a, bool mid, hipStream_t s);
 hipError_t launch_glu_tiles(const FusedArgs& a, bool mid, hipStream_t s);        // its gated part
 hipError_t launch_residual_tiles(const FusedArgs& a, bool mid, hipStream_t s);   // and that with a gate or a residual
 
+// Experts' products (moe_small.hip, moe_tiles.hip): the rows of expert e, as a
+// plan (moe_plan.h) orders them, by weight e of a stack.  g.m rows in all; row p
+// of the result is that of plan row p.
+struct MoeArgs : FusedArgs {
+  const int32_t* tiles[5] = {};       // the plan's tile tables and their lengths
+  const int32_t* ntiles = nullptr;    // [5]
+  const int32_t* token = nullptr;     // row p reads row token[p] of A; null: row p
+  int32_t a_rows = 0;                 // rows of A
+  int32_t experts = 0;
+  int64_t w_codes = 0, w_scales = 0;  // bytes from one expert's weights to the next's
+  // the result as 16-bit values with a power of two per 32 columns (g.y, z_scales)
+  bool z_half = false;
+  uint8_t* z_scales = nullptr;
+};
+
 // Norm with residual, gate and modulation (norm.hip); dense or MXFP4 result.
 struct NormArgs {
   const void* x;
@@ -157,5 +172,50 @@ struct NormArgs {
 constexpr int64_t kNormMaxD = 65536;          // row length
 constexpr int64_t kNormMaxDKron = 16384;      // and with KRON, whose rows pass through LDS
 hipError_t launch_norm(const NormArgs& a, hipStream_t s);
+
+// Mixture of experts (moe_route.hip): router, plan and the weighted sum over a
+// token's choices.
+struct RouteArgs {
+  const void* logits;    // [tokens][ld]
+  const float* bias;     // [experts] or null
+  int32_t* ids;          // [tokens][topk]
+  float* weights;
+  int64_t tokens, ld;
+  int32_t experts, topk, groups, topk_groups;
+  bool bf16, softmax, group_top2, renormalize;
+  float scale;
+};
+hipError_t launch_moe_route(const RouteArgs& a, hipStream_t s);
+
+struct PlanArgs {
+  const int32_t* ids;    // [pairs]
+  int64_t pairs, chunk;
+  int32_t topk, first, experts;
+  int32_t *offsets, *order, *slot, *token, *ntiles, *tiles[5], *counts;
+};
+hipError_t launch_moe_plan(const PlanArgs& a, hipStream_t s);
+
+struct CombineArgs {
+  const void* z;             // [rows][n] fp32, or 16-bit values with z_scales
+  const uint8_t* z_scales;
+  bool half;
+  const int32_t* slot;       // [tokens][topk]
+  const float* weights;
+  const void* residual;      // [tokens][ld_res] or null
+  int64_t ld_res;
+  bool res_bf16;
+  void* y;                   // [tokens][ld_y]
+  int64_t ld_y;
+  bool y_bf16;
+  int64_t tokens;
+  int32_t topk, n;
+};
+hipError_t launch_moe_combine(const CombineArgs& a, hipStream_t s);
+
+// The kernel for the experts' products: row tiles of 16, 32 or 64 (small-M), 128
+// or 256 rows; 0: none.
+int moe_tile_rows(const MoeArgs& f);
+hipError_t launch_moe_small(const MoeArgs& f, int rows, hipStream_t s);
+hipError_t launch_moe_tiles(const MoeArgs& f, bool mid, hipStream_t s);
 
 }  // namespace mxfp4
