@@ -527,7 +527,8 @@ typedef enum {
  * out.  Then the topk largest keys, in descending order, ties to the lowest
  * index, between groups too.  weights = s of the chosen, divided by their sum if
  * renormalize (0 where that sum is 0), times scale.  Scores, keys with a bias and
- * group scores are formed in binary64, weights rounded once.
+ * group scores are formed in binary64 (two s + bias that agree to 2^-42 of their
+ * value count as equal), weights rounded once.
  * Logits of -infinity or NaN are experts that cannot be chosen; a bias of
  * -infinity takes one out as well.  Where fewer than topk can be chosen, the
  * remaining ids are -1 with weight 0. */

@@ -59,6 +59,7 @@ mxfp4_status set_operands(const uint8_t* a_codes, const uint8_t* a_scales, int64
   f.g.k = static_cast<int32_t>(k);
   f.g.tiled = tiled;
   f.a_rows = static_cast<int32_t>(rows);
+  f.a_tiled = tiled;
   f.w_codes = wrows * (k / 2);
   f.w_scales = wrows * (k / 32);
   height = mxfp4::moe_tile_rows(f);

@@ -293,27 +293,38 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(Args f,
     return p;
   };
   uint32_t coff[CODE_LOADS], soff[SCALE_LOADS];
-  auto plan = [&](int j) __attribute__((always_inline)) {
-    const Place at = place(j);
+  const bool a_tiled = MOE ? moe::a_tiled(f) : tiled;
+  // MOE: the rows of A that this lane loads for a tile (activation side).
+  struct Rows { Place at; int code[CODE_LOADS], scale[SCALE_LOADS]; };
+  auto fetch = [&](int j, Rows& t) __attribute__((always_inline)) {
+    t.at = place(j);
+    if (!w_first) {
+#pragma unroll
+      for (int i = 0; i < CODE_LOADS; ++i)
+        t.code[i] = moe::source_row(f, min(t.at.row0 + 16 * code_group(i) - BN + (lane >> 2), t.at.end - 1));
+#pragma unroll
+      for (int i = 0; i < SCALE_LOADS; ++i)
+        t.scale[i] = moe::source_row(f, min(t.at.row0 + 64 * scale_group(i) - BN + lane, t.at.end - 1));
+    }
+  };
+  auto offsets = [&](const Place& at, const Rows& t) __attribute__((always_inline)) {
     const int tn = at.tn;
-    if constexpr (MOE) bases(at.expert * f.w_codes, at.expert * f.w_scales);
+    if constexpr (MOE) bases(at.expert * moe::code_step(f), at.expert * moe::scale_step(f));
 #pragma unroll
     for (int i = 0; i < CODE_LOADS; ++i) {
       const int q = code_group(i);
       const bool w = code_w(i);
       const int row0 = w ? tn * TN + (GLU ? 32 * (q >> 2) + 16 * (q & 1) : 16 * q) : at.row0 + 16 * q - BN;
       if (MOE && !w) {
-        // (a tile's row r lies in a swizzle of its own: the source's is undone)
-        const int in = 16 * q - BN + (lane >> 2);
-        const uint32_t src = (uint32_t)moe::source_row(f, min(at.row0 + in, at.end - 1));
-        const uint32_t chunk = (uint32_t)((lane & 3) ^ swz(in & 255));
-        coff[i] = tiled ? (src >> 8) * nstage * (16 * 1024) + (src & 255) * 64 + 16 * (chunk ^ (uint32_t)swz((int)(src & 255)))
-                        : src * kbytes + 16 * chunk;
+        // (a tile's rows lie in a swizzle of their own: the source's is undone)
+        const uint32_t src = (uint32_t)t.code[i], chunk = (uint32_t)((lane & 3) ^ swz((16 * q - BN + (lane >> 2)) & 255));
+        coff[i] = a_tiled ? (src >> 8) * nstage * (16 * 1024) + (src & 255) * 64 + 16 * (chunk ^ (uint32_t)swz((int)(src & 255)))
+                          : src * kbytes + 16 * chunk;
       } else if (tiled) {
         coff[i] = (uint32_t)(row0 >> 8) * nstage * (16 * 1024) + (uint32_t)(row0 & 255) * 64 + lane * 16;
       } else {
         const int row = row0 + (lane >> 2);
-        const uint32_t grow = (uint32_t)min(row, (w ? g.n : at.end) - 1);
+        const uint32_t grow = (uint32_t)min(row, (w ? g.n : g.m) - 1);
         coff[i] = grow * kbytes + 16u * (uint32_t)((lane & 3) ^ swz(row & 255));
       }
     }
@@ -321,14 +332,30 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(Args f,
     for (int i = 0; i < SCALE_LOADS; ++i) {
       const int q = scale_group(i);
       const bool w = scale_w(i);
-      int row = w ? tn * TN + (GLU ? 32 * q + lr : 64 * q + lane) : at.row0 + 64 * q - BN + lane;
-      if (MOE && !w) row = moe::source_row(f, min(row, at.end - 1));
-      soff[i] = tiled ? (uint32_t)(row >> 8) * nstage * 1024 + (uint32_t)(row & 255) * 4
-                      : (uint32_t)(MOE && !w ? row : min(row, (w ? g.n : at.end) - 1)) * kblocks;
+      const int row = MOE && !w ? t.scale[i] : w ? tn * TN + (GLU ? 32 * q + lr : 64 * q + lane) : at.row0 + 64 * q - BN + lane;
+      soff[i] = (MOE && !w ? a_tiled : tiled) ? (uint32_t)(row >> 8) * nstage * 1024 + (uint32_t)(row & 255) * 4
+                                              : (uint32_t)min(row, (MOE && !w ? row + 1 : w ? g.n : g.m) - 1) * kblocks;
     }
   };
-  const uint32_t cstride = tiled ? 16 * 1024 : RB, sstride = tiled ? 1024 : 4;   // bytes per stage
+  // bytes per stage (MOE: each wave loads one side, of a layout of its own)
+  const bool strided = MOE && !w_first ? a_tiled : tiled;
+  const uint32_t cstride = strided ? 16 * 1024 : RB, sstride = strided ? 1024 : 4;
   int ij = 0, ikt = 0, ibuf = 0;   // issue state: tile, stage within it, ring slot
+  // MOE: a tile's rows are asked for two tiles ahead, in the epilogue, so that
+  // nobody waits for them (and, vector loads arriving in order, for the ring's)
+  // where the ring goes on to it; the ring is one tile ahead of the epilogue at
+  // most if nk >= NBUF - 1.
+  const bool early = MOE && nk >= NBUF - 1;
+  Rows next;
+  auto plan = [&](int j) __attribute__((always_inline)) {
+    if constexpr (MOE) {
+      if (!early || j == 0) fetch(j, next);
+      offsets(next.at, next);
+    } else {
+      offsets(place(j), next);
+    }
+  };
+  static_assert(!MOE || T::WHOLE, "a wave's loads are of one side");
   plan(0);
   auto issue_codes = [&](int i0, int i1) __attribute__((always_inline)) {
     uint8_t* dst = lds + ibuf * STAGE_BYTES;
@@ -398,6 +425,9 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(Args f,
     issue_codes(0, CODE_LOADS);
     issue_scales();
   }, std::make_integer_sequence<int, NBUF - 1>{});
+  if constexpr (MOE) {
+    if (early && nk < total) fetch(1, next);
+  }
   v16f acc[FN][FM];
 #pragma unroll
   for (int a = 0; a < FN; ++a)
@@ -483,6 +513,19 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(Args f,
     // ---- epilogue of this workgroup's j-th tile
     const int mw0 = at.row0 + wm * (BM / WM), nw0 = tn * TN + wn * WCOLS;   // the wave's block of Y
     const bool relu = f.act == act::RELU;
+    const bool more = early && (j + 2) * nk < total;
+    if constexpr (MOE) {
+      if (more) fetch(j + 2, next);
+    }
+    // next's loads have arrived: called ahead of the epilogue's first stores
+    auto settle = [&]() __attribute__((always_inline)) {
+      if constexpr (MOE) {
+#pragma unroll
+        for (int i = 0; i < CODE_LOADS; ++i) asm volatile("" : "+v"(next.code[i]));
+#pragma unroll
+        for (int i = 0; i < SCALE_LOADS; ++i) asm volatile("" : "+v"(next.scale[i]));
+      }
+    };
     constexpr int NO = GLU ? FN / 2 : FN;   // output fragments along N
 
     // The bias onto the i-th output fragment, in the order in which they leave.
@@ -554,6 +597,7 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(Args f,
         for (int o = 0; o < NO; ++o) {
           float v[16];
           take(o, bb, v);
+          if (o == 0 && bb == 0) settle();
           if (f.h32) hadamard_fragment(v);
           float am = 0.0f;
 #pragma unroll
@@ -709,6 +753,7 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(Args f,
             }
           }
         }
+        if constexpr (p == 0) settle();
         // the area is private to this wave: its LDS writes land before its reads
         auto staged = [&](int r) {
           const int row = RPI * r + prow;

@@ -135,6 +135,7 @@ struct MoeArgs : FusedArgs {
   const int32_t* ntiles = nullptr;    // [5]
   const int32_t* token = nullptr;     // row p reads row token[p] of A; null: row p
   int32_t a_rows = 0;                 // rows of A
+  bool a_tiled = false;               // A's layout (g.tiled: the weights')
   int32_t experts = 0;
   int64_t w_codes = 0, w_scales = 0;  // bytes from one expert's weights to the next's
   // the result as 16-bit values with a power of two per 32 columns (g.y, z_scales)

@@ -29,13 +29,13 @@ inline int64_t max_tiles(int64_t pairs, int64_t experts, int64_t rows) {
   return pairs / rows + (experts < pairs ? experts : pairs);
 }
 
-// Pairs per workgroup of the sort: one workgroup up to 4096 of them, then 1024
-// each on up to 128 workgroups (each of them adds up the others' counts).
-constexpr int64_t kOneChunk = 4096;
+// Pairs per workgroup of the sort: one workgroup up to kOneChunk of them, then
+// 1024 each on up to 128 workgroups (each of them adds up the others' counts).
+constexpr int64_t kOneChunk = 8192;
 inline int64_t chunk_pairs(int64_t pairs) {
   if (pairs <= kOneChunk) return kOneChunk;
   const int64_t c = (pairs + 127) / 128;
-  return c <= 1024 ? 1024 : (c + 511) / 512 * 512;
+  return c <= 1024 ? 1024 : (c + 1023) / 1024 * 1024;
 }
 inline int64_t chunks(int64_t pairs) {
   const int64_t c = chunk_pairs(pairs);

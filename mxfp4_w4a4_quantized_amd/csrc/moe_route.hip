@@ -6,216 +6,279 @@
 namespace mxfp4 {
 namespace {
 
-constexpr double kNone = -__builtin_inf();   // key of an expert that cannot be chosen
-
 // ---------------------------------------------------------------------------
 // Router.  Token t's scores s = softmax(l) or sigmoid(l); its choices are the
 // topk experts with the largest key, ties to the lowest index; its weights are
 // their scores, divided by their sum if asked, times a scale.
 //
-// Keys.  Without a bias the logits themselves: the scores' order before any
-// rounding.  With a bias s + bias in 64 bits, where two experts next to each
-// other on the border of the choice stay apart; so are the sums of a group's two
-// best.  A 64-bit exponential per logit costs less than the launch.
+// Keys are 64-bit floats: without a bias the logits themselves, the scores' order
+// before any rounding; with one s + bias, where two experts next to each other on
+// the border of the choice stay apart.  The expert's index is put into a key's ten
+// lowest bits (which a logit leaves empty, and s + bias has at 2^-42 of its value),
+// so that one maximum finds the expert and settles ties.
 //
-// A wave per token, expert 64 i + lane in register i: a choice is a maximum over
-// a lane's registers, then over the lanes by DPP moves; equal keys, which bf16
-// logits often have, are settled by the smallest index among the lanes that hold
-// the maximum.  Groups: the keys pass through LDS, lane g scans group g, and a
-// group's rank among the others says whether it is kept.
+// G lanes serve a token, expert G i + lane of them in register i.  64 lanes give
+// the shortest time for few tokens; for many, 16 lanes: of the instructions of a
+// choice those between lanes are then shared by four tokens (8192 tokens x 256
+// experts, sigmoid, bias, groups: @ROUTE@).  What remains is the 64-bit arithmetic
+// of an exponential and a reciprocal for each score.
 
-// The maximum over the wave, by row shifts and row broadcasts (in lane 63).
-template <int CTRL>
-__device__ __forceinline__ double dpp_max(double v) {
-  const uint64_t u = (uint64_t)__builtin_bit_cast(uint64_t, v);
-  const int lo = (int)(uint32_t)u, hi = (int)(uint32_t)(u >> 32);
-  const uint32_t l2 = (uint32_t)__builtin_amdgcn_update_dpp(lo, lo, CTRL, 0xf, 0xf, false);
-  const uint32_t h2 = (uint32_t)__builtin_amdgcn_update_dpp(hi, hi, CTRL, 0xf, 0xf, false);
-  return fmax(v, __builtin_bit_cast(double, ((uint64_t)h2 << 32) | l2));
+// Below every key: none is left.  Keys are kept within +-1e308.
+constexpr uint32_t kNoneHigh = 0xFFEFFFFFu;   // of -1.79e308
+__device__ __forceinline__ double none() { return __builtin_bit_cast(double, (uint64_t)kNoneHigh << 32); }
+__device__ __forceinline__ bool is_none(double k) { return (uint32_t)(__builtin_bit_cast(uint64_t, k) >> 32) == kNoneHigh; }
+
+constexpr int kIndexBits = 10;
+static_assert((1 << kIndexBits) >= moe::kMaxExperts, "an expert's index fits");
+
+__device__ __forceinline__ double pack_key(double v, int e) {
+  v = v > 1e308 ? 1e308 : v < -1e308 ? -1e308 : v + 0.0;   // (+ 0.0: one zero)
+  const uint64_t u = __builtin_bit_cast(uint64_t, v), mask = (1 << kIndexBits) - 1;
+  const uint64_t low = (u >> 63) ? e : mask - e;            // the lower index is the larger key
+  return __builtin_bit_cast(double, (u & ~mask) | low);
 }
-template <int CTRL>
-__device__ __forceinline__ float dpp_max(float v) {
-  const int u = __float_as_int(v);
-  return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(u, u, CTRL, 0xf, 0xf, false)));
+__device__ __forceinline__ int key_index(double k) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, k);
+  const int mask = (1 << kIndexBits) - 1, low = (int)u & mask;
+  return (u >> 63) ? low : mask - low;
 }
-__device__ __forceinline__ float lane_value(float v, int lane) {
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+__device__ __forceinline__ double key_value(double k) {
+  return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, k) & ~(uint64_t)((1 << kIndexBits) - 1));
 }
-__device__ __forceinline__ double lane_value(double v, int lane) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
-  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
-}
+
+// The larger of two (no NaN here: a select costs less than a NaN-safe maximum).
 template <typename T>
-__device__ __forceinline__ T wave_max(T v) {
-  v = dpp_max<0x111>(v);   // row_shr:1, 2, 4, 8
-  v = dpp_max<0x112>(v);
-  v = dpp_max<0x114>(v);
-  v = dpp_max<0x118>(v);
-  v = dpp_max<0x142>(v);   // row_bcast:15, 31
-  v = dpp_max<0x143>(v);
-  return lane_value(v, 63);
+__device__ __forceinline__ T larger(T a, T b) { return a > b ? a : b; }
+
+// v of the lane that a row rotation or a swap of rows or halves brings here.
+template <int CTRL>
+__device__ __forceinline__ uint32_t rotated(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
 }
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+template <int CTRL>
+__device__ __forceinline__ double rotated(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, ((uint64_t)rotated<CTRL>((uint32_t)(u >> 32)) << 32) | rotated<CTRL>((uint32_t)u));
+}
+template <int CTRL>
+__device__ __forceinline__ float rotated(float v) { return __uint_as_float(rotated<CTRL>(__float_as_uint(v))); }
+
+struct Max {
+  template <typename T> __device__ __forceinline__ T operator()(T a, T b) const { return larger(a, b); }
+};
+struct Sum {
+  template <typename T> __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
+};
+
+// op over the G lanes of a token, in every one of them: rotations within rows of
+// 16, then rows and halves of the wave swapped.
+template <int G, class Op, typename T>
+__device__ __forceinline__ T across(T v, Op op) {
+  v = op(v, rotated<0x128>(v));   // row_ror:8, 4, 2, 1
+  v = op(v, rotated<0x124>(v));
+  v = op(v, rotated<0x122>(v));
+  v = op(v, rotated<0x121>(v));
+  if constexpr (G == 64) {
+    v = op(__shfl_xor(v, 16), v);
+    v = op(__shfl_xor(v, 32), v);
+  }
   return v;
+}
+
+// e^x in 64 bits, relative error some 2^-47: x = n ln 2 + r, |r| <= ln 2 / 2, with
+// ln 2 in two parts (Cody and Waite), and the series of e^r to r^11.  0 below -700.
+__device__ __forceinline__ double exp64(double x) {
+  const double n = __builtin_rint(x * 1.4426950408889634);
+  const double r = __builtin_fma(n, -1.9082149292705877e-10, __builtin_fma(n, -0.69314718036912382, x));
+  double p = 1.0 / 39916800;
+  p = __builtin_fma(p, r, 1.0 / 3628800);
+  p = __builtin_fma(p, r, 1.0 / 362880);
+  p = __builtin_fma(p, r, 1.0 / 40320);
+  p = __builtin_fma(p, r, 1.0 / 5040);
+  p = __builtin_fma(p, r, 1.0 / 720);
+  p = __builtin_fma(p, r, 1.0 / 120);
+  p = __builtin_fma(p, r, 1.0 / 24);
+  p = __builtin_fma(p, r, 1.0 / 6);
+  p = __builtin_fma(p, r, 0.5);
+  p = __builtin_fma(p, r, 1.0);
+  p = __builtin_fma(p, r, 1.0);
+  return x < -700.0 ? 0.0 : __builtin_ldexp(p, (int)n);
+}
+// 1 / x by two Newton steps on the instruction's 2^-14 or better (x normal).
+__device__ __forceinline__ double rcp64(double x) {
+  double r = __builtin_amdgcn_rcp(x);
+  r = __builtin_fma(__builtin_fma(-x, r, 1.0), r, r);
+  return __builtin_fma(__builtin_fma(-x, r, 1.0), r, r);
+}
+__device__ __forceinline__ double sigmoid64(double x) {
+  const double e = exp64(-__builtin_fabs(x)), r = rcp64(1.0 + e);
+  return x < 0.0 ? e * r : r;
 }
 
 constexpr int kRouteWaves = 4;
 
-// NV: experts per lane.  Key: float (the logits) or double (score + bias).
-template <int NV, typename Key>
+template <int G, int NV, bool BIAS, bool GROUPS>
 __global__ __launch_bounds__(64 * kRouteWaves) void moe_route_kernel(RouteArgs a) {
-  extern __shared__ double lds_keys[];   // [kRouteWaves][experts], with groups
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
-  if (t >= a.tokens) return;   // (no barrier below: a wave works alone)
-  constexpr bool kBias = sizeof(Key) == 8;
+  extern __shared__ double lds[];   // GROUPS: [tokens][experts + groups + 1], then [tokens][64]
+  constexpr int PER = 64 * kRouteWaves / G;   // tokens of a workgroup
+  const int sub = threadIdx.x % G, slot = threadIdx.x / G;
+  const int64_t t0 = (int64_t)blockIdx.x * PER + slot;
+  const bool live = t0 < a.tokens;
+  const int64_t t = live ? t0 : a.tokens - 1;   // (idle lanes repeat the last token: barriers and lane moves stay whole)
   const float kInf = __builtin_inff();
 
-  float x[NV];
+  auto logit = [&](int e) {
+    const float v = a.bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.logits)[t * a.ld + e] << 16)
+                           : static_cast<const float*>(a.logits)[t * a.ld + e];
+    return v > -kInf ? v : -kInf;   // NaN is no candidate either
+  };
+  float x[NV], bias[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = 64 * i + lane;
-    x[i] = -kInf;
-    if (e < a.experts) {
-      if (a.bf16) x[i] = __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.logits)[t * a.ld + e] << 16);
-      else x[i] = static_cast<const float*>(a.logits)[t * a.ld + e];
-    }
-    if (!(x[i] > -kInf)) x[i] = -kInf;   // NaN is no candidate either
+    const int e = G * i + sub;
+    x[i] = e < a.experts ? logit(e) : -kInf;
+    if constexpr (BIAS) bias[i] = e < a.experts ? a.bias[e] : 0.0f;
   }
-  float bias[NV];
-  if constexpr (kBias) {
+  float top = x[0];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) bias[i] = 64 * i + lane < a.experts ? a.bias[64 * i + lane] : 0.0f;
-  }
+  for (int i = 1; i < NV; ++i) top = larger(top, x[i]);
+  if (a.softmax) top = across<G>(top, Max());
 
-  // scores in 64 bits
-  double s[NV];
-  if (a.softmax) {
-    float top = x[0];
-#pragma unroll
-    for (int i = 1; i < NV; ++i) top = fmaxf(top, x[i]);
-    top = wave_max(top);
+  // The scores that are needed before the choice: all of them for keys with a
+  // bias and for groups, and for the sum that a softmax is divided by.
+  constexpr bool ALL = BIAS || GROUPS;
+  double s[ALL ? NV : 1], scale = 1.0;
+  if (ALL || (a.softmax && !a.renormalize)) {
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      s[i] = x[i] > -kInf ? exp((double)x[i] - (double)top) : 0.0;
-      sum += s[i];
+      double v = 0.0;
+      if (a.softmax) v = exp64((double)x[i] - (double)top);
+      else if constexpr (ALL) v = sigmoid64((double)x[i]);
+      v = x[i] > -kInf ? v : 0.0;
+      sum += v;
+      if constexpr (ALL) s[i] = v;
     }
-    sum = wave_sum(sum);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) s[i] = s[i] / sum;
-  } else {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) s[i] = x[i] > -kInf ? 1.0 / (1.0 + exp(-(double)x[i])) : 0.0;
+    if (a.softmax) scale = 1.0 / across<G>(sum, Sum());
   }
-
-  Key key[NV];
+  double key[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    if constexpr (kBias) {
-      const double c = s[i] + (double)bias[i];
-      key[i] = x[i] > -kInf && c > kNone ? c : kNone;
-    } else {
-      key[i] = x[i];
-    }
+    double v = (double)x[i];
+    if constexpr (BIAS) v = s[i] * scale + (double)bias[i];
+    const bool can = x[i] > -kInf && v > -(double)kInf;
+    key[i] = can ? pack_key(v, G * i + sub) : none();
   }
 
-  if (a.groups > 1) {
-    double* mine = lds_keys + (int64_t)wave * a.experts;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (64 * i + lane < a.experts) mine[64 * i + lane] = key[i] > (Key)kNone ? (kBias ? (double)key[i] : s[i]) : kNone;
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    const int size = a.experts / a.groups;
-    double first = kNone, second = kNone;
-    if (lane < a.groups) {
-      int at = lane % size;   // lanes start apart: other LDS banks
-      for (int i = 0; i < size; ++i) {
-        const double v = mine[lane * size + at];
-        second = fmax(second, fmin(first, v));
-        first = fmax(first, v);
-        at = at + 1 == size ? 0 : at + 1;
-      }
-    }
-    // a group's score: its best key, or the sum of its two best (of one where it has one)
-    const double score = a.group_top2 && second > kNone ? first + second : first;
-    int rank = 0;
-    for (int g = 0; g < a.groups; ++g) {
-      const double other = lane_value(score, g);
-      rank += other > score || (other == score && g < lane) ? 1 : 0;
-    }
-    const uint64_t kept = __builtin_amdgcn_ballot_w64(lane < a.groups && rank < a.topk_groups);
+  if constexpr (GROUPS) {
+    // Lane sub scans a part of group sub / L; a group is a run of experts, one
+    // double apart from the next in LDS (other banks).
+    const int size = a.experts / a.groups, stride = a.experts + a.groups + 1;
+    const float per = 1.0f / (float)size;
+    auto group_of = [&](int e) { return (int)(((float)e + 0.5f) * per); };
+    double* mine = lds + slot * stride;
+    double* scores = lds + PER * stride + slot * 64;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = 64 * i + lane;
-      if (e < a.experts && !((kept >> (e / size)) & 1)) key[i] = (Key)kNone;
+      const int e = G * i + sub;
+      if (e < a.experts) mine[e + group_of(e)] = is_none(key[i]) ? none() : BIAS ? key_value(key[i]) : s[i];
     }
-  }
-
-  // lane j keeps choice j
-  int id = -1;
-  double chosen = 0.0;
-  for (int j = 0; j < a.topk; ++j) {
-    Key best = key[0];
-    int at = 0;
-#pragma unroll
-    for (int i = 1; i < NV; ++i) {
-      at = key[i] > best ? i : at;
-      best = key[i] > best ? key[i] : best;
+    __syncthreads();
+    int L = 1;
+    while (2 * L * a.groups <= G && 2 * L <= size) L *= 2;
+    for (int g0 = 0; g0 < a.groups; g0 += G / L) {
+      const int g = g0 + sub / L, part = sub % L;
+      double first = none(), second = none();
+      if (g < a.groups) {
+        const double* p = mine + g * (size + 1);
+        for (int i = part; i < size; i += L) {
+          const double v = p[i];
+          second = larger(second, first < v ? first : v);
+          first = larger(first, v);
+        }
+      }
+      for (int d = 1; d < L; d *= 2) {
+        const double f2 = __shfl_xor(first, d), s2 = __shfl_xor(second, d);
+        second = larger(larger(second, s2), first < f2 ? first : f2);
+        first = larger(first, f2);
+      }
+      // its best key, or the sum of its two best (of one where it has one)
+      if (part == 0 && g < a.groups) scores[g] = a.group_top2 && !is_none(second) ? first + second : first;
     }
-    const Key top = wave_max(best);
-    if (!(top > (Key)kNone)) break;
-    uint64_t who = __builtin_amdgcn_ballot_w64(best == top);
-    const int mine = 64 * at + lane;
-    int e = __builtin_amdgcn_readlane(mine, __builtin_ctzll(who));
-    for (who &= who - 1; who != 0; who &= who - 1) e = min(e, __builtin_amdgcn_readlane(mine, __builtin_ctzll(who)));
-    double score = 0.0;
+    __syncthreads();
+    uint64_t kept = 0;
+    for (int g0 = 0; g0 < a.groups; g0 += G) {
+      const int g = g0 + sub;
+      const double score = g < a.groups ? scores[g] : none();
+      int rank = 0;
+      for (int h = 0; h < a.groups; ++h) {
+        const double other = scores[h];
+        rank += other > score || (other == score && h < g) ? 1 : 0;
+      }
+      const uint64_t in = __builtin_amdgcn_ballot_w64(g < a.groups && rank < a.topk_groups);
+      kept |= G == 64 ? in : ((in >> (threadIdx.x & 48)) & 0xFFFFu) << g0;
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (64 * i + lane == e) {
-        score = s[i];
-        key[i] = (Key)kNone;
-      }
-    score = lane_value(score, e & 63);
-    if (lane == j) {
-      id = e;
-      chosen = score;
+      if (!((kept >> (group_of(G * i + sub) & 63)) & 1)) key[i] = none();   // (no expert: none already)
+  }
+
+  // lane j of the token keeps choice j
+  int id = -1;
+  for (int j = 0; j < a.topk; ++j) {
+    double best = key[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) best = larger(best, key[i]);
+    best = across<G>(best, Max());
+    const uint64_t b = __builtin_bit_cast(uint64_t, best);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint64_t u = __builtin_bit_cast(uint64_t, key[i]);
+      key[i] = u == b ? none() : key[i];
     }
+    if (sub == j) id = is_none(best) ? -1 : key_index(best);
+  }
+  double w = 0.0;
+  if (id >= 0) {
+    const double l = (double)logit(id);
+    w = a.softmax ? exp64(l - (double)top) * scale : sigmoid64(l);
   }
   if (a.renormalize) {
-    const double sum = wave_sum(chosen);
-    chosen = sum > 0.0 ? chosen / sum : sum != sum ? sum : 0.0;
+    const double sum = across<G>(w, Sum());
+    w = sum == 0.0 ? 0.0 : w / sum;
   }
-  if (lane < a.topk) {
-    a.ids[t * a.topk + lane] = id;
-    a.weights[t * a.topk + lane] = id < 0 ? 0.0f : (float)(chosen * (double)a.scale);
+  if (live && sub < a.topk) {
+    a.ids[t * a.topk + sub] = id;
+    a.weights[t * a.topk + sub] = (float)(w * (double)a.scale);
   }
 }
 
-template <int NV>
+template <int G, int NV>
 void launch_route_nv(const RouteArgs& a, hipStream_t s) {
-  const int grid = (int)((a.tokens + kRouteWaves - 1) / kRouteWaves);
-  const size_t lds = a.groups > 1 ? sizeof(double) * kRouteWaves * a.experts : 0;
-  if (a.bias != nullptr) moe_route_kernel<NV, double><<<grid, 64 * kRouteWaves, lds, s>>>(a);
-  else moe_route_kernel<NV, float><<<grid, 64 * kRouteWaves, lds, s>>>(a);
+  constexpr int PER = 64 * kRouteWaves / G;
+  const int grid = (int)((a.tokens + PER - 1) / PER);
+  const size_t bytes = sizeof(double) * PER * (a.experts + a.groups + 1 + 64);
+  if (a.groups > 1) {
+    if (a.bias != nullptr) moe_route_kernel<G, NV, true, true><<<grid, 64 * kRouteWaves, bytes, s>>>(a);
+    else moe_route_kernel<G, NV, false, true><<<grid, 64 * kRouteWaves, bytes, s>>>(a);
+  } else {
+    if (a.bias != nullptr) moe_route_kernel<G, NV, true, false><<<grid, 64 * kRouteWaves, 0, s>>>(a);
+    else moe_route_kernel<G, NV, false, false><<<grid, 64 * kRouteWaves, 0, s>>>(a);
+  }
 }
 
 // ---------------------------------------------------------------------------
 // Plan: a stable counting sort of the pairs by expert, on integers only (the
-// same plan on every run).  Up to 4096 pairs one workgroup does it in one launch.
-// Beyond that moe_count_kernel counts each chunk's pairs by expert, and in
-// moe_place_kernel every workgroup adds up the counts of all chunks and of those
-// before its own.  Within a chunk a wave takes a run of pairs, 64 at a time: the
-// lanes with the same expert are found with a ballot for each bit of its number,
-// and a lane's place among them is a bit count.
+// same plan on every run).  Up to kOneChunk pairs one workgroup does it in one
+// launch.  Beyond that moe_count_kernel counts each chunk's pairs by expert, and
+// in moe_place_kernel every workgroup adds up the counts of all chunks and of
+// those before its own.  Within a chunk a wave takes a run of pairs, 64 at a time:
+// the lanes with the same expert are found with a ballot for each bit of its
+// number, and a lane's place among them is a bit count.  Bound by latency: the
+// ids, then LDS round trips between barriers.
 
-constexpr int kPlanWaves = 8;
+constexpr int kPlanWaves = 16;
+constexpr int kHeld = 8;   // steps of 64 pairs whose ids a wave reads once
 
 __device__ __forceinline__ int expert_of(const PlanArgs& a, int64_t p, int64_t end) {
   if (p >= end) return -1;
@@ -228,6 +291,7 @@ __global__ __launch_bounds__(64 * kPlanWaves) void moe_count_kernel(PlanArgs a) 
   for (int e = threadIdx.x; e < a.experts; e += blockDim.x) cnt[e] = 0;
   __syncthreads();
   const int64_t begin = blockIdx.x * a.chunk, end = min(a.pairs, begin + a.chunk);
+#pragma unroll 4
   for (int64_t p = begin + threadIdx.x; p < end; p += blockDim.x) {
     const int e = expert_of(a, p, end);
     if (e >= 0) atomicAdd(&cnt[e], 1);
@@ -236,12 +300,14 @@ __global__ __launch_bounds__(64 * kPlanWaves) void moe_count_kernel(PlanArgs a) 
   for (int e = threadIdx.x; e < a.experts; e += blockDim.x) a.counts[blockIdx.x * (int64_t)a.experts + e] = cnt[e];
 }
 
-__device__ __forceinline__ int wave_scan(int v, int lane) {   // inclusive
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
+// Inclusive sum over the wave: row shifts, then row broadcasts.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);   // row_shr:1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31 into rows 2 and 3
   return v;
 }
 
@@ -250,29 +316,46 @@ __global__ __launch_bounds__(64 * kPlanWaves) void moe_place_kernel(PlanArgs a) 
   __shared__ int32_t total[moe::kMaxExperts], before[moe::kMaxExperts];
   __shared__ int32_t offset[moe::kMaxExperts + 1];
   __shared__ int32_t first[moe::kHeights][moe::kMaxExperts + 1];   // tiles of each height before an expert's
+  __shared__ int32_t most;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int E = a.experts;
+  const int64_t chunk0 = blockIdx.x * a.chunk, left = a.pairs - chunk0;
+  const int64_t here = left < a.chunk ? left : a.chunk;                         // pairs of this workgroup
+  const int64_t run = (here + 64 * kPlanWaves - 1) / (64 * kPlanWaves) * 64;    // and of a wave
+  const int64_t begin = chunk0 + wave * run, end = min(chunk0 + here, begin + run);
+  int held[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) held[i] = expert_of(a, begin + 64 * i + lane, end);
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
     total[e] = before[e] = 0;
 #pragma unroll
     for (int w = 0; w < kPlanWaves; ++w) pos[w][e] = 0;
   }
+  if (threadIdx.x == 0) most = 0;
   __syncthreads();
-  const int64_t run = a.chunk / kPlanWaves;   // a multiple of 64
-  const int64_t begin = blockIdx.x * a.chunk + wave * run, end = min(a.pairs, begin + run);
-  for (int64_t p = begin + lane; p < end; p += 64) {
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (held[i] >= 0) atomicAdd(&pos[wave][held[i]], 1);
+  for (int64_t p = begin + 64 * kHeld + lane; p < end; p += 64) {
     const int e = expert_of(a, p, end);
     if (e >= 0) atomicAdd(&pos[wave][e], 1);
   }
   if (gridDim.x > 1) {
-    // threads over (chunk, expert) with the experts contiguous
-    const int64_t n = (int64_t)gridDim.x * E;
-    for (int64_t i = threadIdx.x; i < n; i += blockDim.x) {
-      const int c = a.counts[i];
-      const int g = (int)(i / E), e = (int)(i - (int64_t)g * E);
-      if (c != 0) {
-        atomicAdd(&total[e], c);
-        if (g < (int)blockIdx.x) atomicAdd(&before[e], c);
+    // a thread adds up one expert's counts over a part of the chunks
+    const int grid = (int)gridDim.x;
+    for (int e0 = 0; e0 < E; e0 += blockDim.x) {
+      const int wide = min(E - e0, (int)blockDim.x), parts = (int)blockDim.x / wide;
+      const int part = (int)threadIdx.x / wide, e = e0 + (int)threadIdx.x - part * wide;
+      if (part < parts) {
+        int all = 0, mine = 0;
+#pragma unroll 8
+        for (int g = part; g < grid; g += parts) {
+          const int c = a.counts[(int64_t)g * E + e];
+          all += c;
+          mine += g < (int)blockIdx.x ? c : 0;
+        }
+        atomicAdd(&total[e], all);
+        atomicAdd(&before[e], mine);
       }
     }
   }
@@ -290,15 +373,17 @@ __global__ __launch_bounds__(64 * kPlanWaves) void moe_place_kernel(PlanArgs a) 
   if (wave <= moe::kHeights) {
     int32_t* out = wave == 0 ? offset : first[wave - 1];
     const int shift = wave == 0 ? 0 : 3 + wave;   // 16 << h rows
-    int carry = 0;
+    int carry = 0, top = 0;
     for (int e0 = 0; e0 < E; e0 += 64) {
       const int e = e0 + lane;
       const int c = e < E ? (total[e] + (1 << shift) - 1) >> shift : 0;
-      const int v = wave_scan(c, lane);
+      const int v = wave_scan(c);
       if (e < E) out[e] = carry + v - c;
-      carry += __shfl(v, 63);
+      carry += __builtin_amdgcn_readlane(v, 63);
+      top = max(top, c);
     }
     if (lane == 0) out[E] = carry;
+    if (wave == 1) atomicMax(&most, top);
   }
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
@@ -314,9 +399,7 @@ __global__ __launch_bounds__(64 * kPlanWaves) void moe_place_kernel(PlanArgs a) 
 
   const int bits = E > 1 ? 32 - __builtin_clz(E - 1) : 0;
   const uint64_t below = (uint64_t(1) << lane) - 1;
-  for (int64_t p0 = begin; p0 < end; p0 += 64) {
-    const int64_t p = p0 + lane;
-    const int e = expert_of(a, p, end);
+  auto place = [&](int64_t p, int e) {   // 64 pairs in their order
     uint64_t same = __builtin_amdgcn_ballot_w64(e >= 0);
     for (int b = 0; b < bits; ++b) {
       const bool set = (e >> b) & 1;
@@ -334,7 +417,11 @@ __global__ __launch_bounds__(64 * kPlanWaves) void moe_place_kernel(PlanArgs a) 
     }
     __builtin_amdgcn_wave_barrier();
     if (p < end) a.slot[p] = row;
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (begin + 64 * i < end) place(begin + 64 * i + lane, held[i]);
+  for (int64_t p0 = begin + 64 * kHeld; p0 < end; p0 += 64) place(p0 + lane, expert_of(a, p0 + lane, end));
 
   // behind the last row, the offsets and the tile tables: shared out over the grid
   const int64_t tid = blockIdx.x * (int64_t)blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * blockDim.x;
@@ -344,17 +431,28 @@ __global__ __launch_bounds__(64 * kPlanWaves) void moe_place_kernel(PlanArgs a) 
   }
   for (int64_t e = tid; e <= E; e += step) a.offsets[e] = offset[e];
   if (tid < moe::kHeights) a.ntiles[tid] = first[tid][E];
+  auto entry = [&](int h, int i, int e) {
+    reinterpret_cast<int4*>(a.tiles[h])[i] = make_int4(e, offset[e], offset[e + 1], first[h][e]);
+  };
+  if (gridDim.x == 1 && most <= 8) {
+    // few tiles each: a thread per expert and height writes them
+    for (int i = threadIdx.x; i < moe::kHeights * E; i += blockDim.x) {
+      const int h = i / E, e = i - h * E;
+      for (int k = first[h][e]; k < first[h][e + 1]; ++k) entry(h, k, e);
+    }
+  } else {
 #pragma unroll
-  for (int h = 0; h < moe::kHeights; ++h) {
-    const int n = first[h][E];
-    for (int64_t i = tid; i < n; i += step) {
-      int lo = 0, hi = E - 1;   // the last expert whose first tile is at most i, among those with tiles
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (first[h][mid] <= i) lo = mid;
-        else hi = mid - 1;
+    for (int h = 0; h < moe::kHeights; ++h) {
+      const int n = first[h][E];
+      for (int64_t i = tid; i < n; i += step) {
+        int lo = 0, hi = E - 1;   // the last expert whose first tile is at most i: the one with tile i
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (first[h][mid] <= i) lo = mid;
+          else hi = mid - 1;
+        }
+        entry(h, (int)i, lo);
       }
-      reinterpret_cast<int4*>(a.tiles[h])[i] = make_int4(lo, offset[lo], offset[lo + 1], first[h][lo]);
     }
   }
 }
@@ -457,16 +555,17 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(CombineArgs a) {
 }  // namespace
 
 hipError_t launch_moe_route(const RouteArgs& a, hipStream_t s) {
-  switch ((a.experts + 63) / 64) {
-    case 1: launch_route_nv<1>(a, s); break;
-    case 2: launch_route_nv<2>(a, s); break;
-    case 3:
-    case 4: launch_route_nv<4>(a, s); break;
-    case 5:
-    case 6:
-    case 7:
-    case 8: launch_route_nv<8>(a, s); break;
-    default: launch_route_nv<16>(a, s); break;
+  const int e = a.experts;
+  if (a.tokens >= 2048 && e <= 256 && a.topk <= 16) {
+    if (e <= 64) launch_route_nv<16, 4>(a, s);
+    else if (e <= 128) launch_route_nv<16, 8>(a, s);
+    else launch_route_nv<16, 16>(a, s);
+  } else {
+    if (e <= 64) launch_route_nv<64, 1>(a, s);
+    else if (e <= 128) launch_route_nv<64, 2>(a, s);
+    else if (e <= 256) launch_route_nv<64, 4>(a, s);
+    else if (e <= 512) launch_route_nv<64, 8>(a, s);
+    else launch_route_nv<64, 16>(a, s);
   }
   return hipGetLastError();
 }

@@ -36,6 +36,13 @@ __device__ __forceinline__ int enter_tile(const MoeArgs& a, FusedArgs& f, const 
 
 // Row of A that row p of the result reads: with experts, the plan's token.
 __device__ __forceinline__ int source_row(const FusedArgs&, int p) { return p; }
+// The layout of A, and the bytes from one expert's weights to the next's.
+__device__ __forceinline__ bool a_tiled(const FusedArgs& a) { return a.g.tiled; }
+__device__ __forceinline__ bool a_tiled(const MoeArgs& a) { return a.a_tiled; }
+__device__ __forceinline__ int64_t code_step(const FusedArgs&) { return 0; }
+__device__ __forceinline__ int64_t code_step(const MoeArgs& a) { return a.w_codes; }
+__device__ __forceinline__ int64_t scale_step(const FusedArgs&) { return 0; }
+__device__ __forceinline__ int64_t scale_step(const MoeArgs& a) { return a.w_scales; }
 __device__ __forceinline__ int source_row(const MoeArgs& a, int p) { return a.token != nullptr ? a.token[p] : p; }
 
 }  // namespace moe

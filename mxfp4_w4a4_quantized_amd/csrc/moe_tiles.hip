@@ -4,13 +4,28 @@
 namespace mxfp4 {
 
 // The height of the row tiles, by the mean number of rows of an expert.
+//  * Up to 10 rows 16, up to 20 rows 32: the weights are streamed once or nearly,
+//    at 6 to 7.5 TB/s (64 tokens x 8 of 128 experts, 4096 -> 2 x 2048: 148 us in
+//    tiles of 16 rows, 191 in tiles of 128; 256 tokens 185 in 32, 208 in 128; 512
+//    tokens 259 in 32, 221 in 128).
+//  * Then the tile kernels where k allows them (64 rows otherwise), by fused_route's
+//    model of their times on the tiles to expect, half a tile more for each expert
+//    than its rows fill (1024 tokens x 8 of 64 experts, 2048 -> 4096: 113 us in
+//    tiles of 128, 142 in 256; 1024 x 2 of 8 experts, 14336 -> 4096: 130 and 103).
+// It depends on the sizes alone, so dense and MXFP4 outputs of a shape come from the
+// same sums.
 int moe_tile_rows(const MoeArgs& f) {
-  const int64_t mean = f.g.m / f.experts;
-  const bool tiles = f.g.k % large::KS == 0;
-  if (mean <= 12) return 16;
-  if (mean <= 24) return 32;
-  if (mean <= 48 || !tiles) return 64;
-  return mean <= 512 ? 128 : 256;
+  const GemmArgs& g = f.g;
+  const int64_t mean = g.m / f.experts;
+  if (mean <= 10) return 16;
+  if (mean <= 20) return 32;
+  if (g.k % large::KS != 0) return 64;
+  const int64_t cus = cu_count(), nk = g.k / large::KS, wide = f.glu ? 2 * int64_t(g.n) : g.n;
+  auto tiles = [&](int64_t t) { return (g.m / t + (f.experts + 1) / 2) * ((wide + t - 1) / t); };
+  const int64_t t256 = tiles(256), t128 = tiles(128), rest = t128 % (2 * cus);
+  const int64_t c256 = (t256 + cus - 1) / cus * (5 * nk + 120);
+  const int64_t c128 = t128 / (2 * cus) * (5 * nk + 50) + (rest == 0 ? 0 : (rest <= cus ? 3 * nk : 5 * nk) + 50);
+  return c128 < c256 ? 128 : 256;
 }
 
 hipError_t launch_moe_tiles(const MoeArgs& f, bool mid, hipStream_t s) {
