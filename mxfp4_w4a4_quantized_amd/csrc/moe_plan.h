@@ -31,7 +31,7 @@ inline int64_t max_tiles(int64_t pairs, int64_t experts, int64_t rows) {
 
 // Pairs per workgroup of the sort: one workgroup up to kOneChunk of them, then
 // 1024 each on up to 128 workgroups (each of them adds up the others' counts).
-constexpr int64_t kOneChunk = 8192;
+constexpr int64_t kOneChunk = 4096;
 inline int64_t chunk_pairs(int64_t pairs) {
   if (pairs <= kOneChunk) return kOneChunk;
   const int64_t c = (pairs + 127) / 128;

@@ -278,6 +278,7 @@ void launch_route_nv(const RouteArgs& a, hipStream_t s) {
 // ids, then LDS round trips between barriers.
 
 constexpr int kPlanWaves = 16;
+static_assert(64 * kPlanWaves >= moe::kMaxExperts, "a thread for each expert");
 constexpr int kHeld = 8;   // steps of 64 pairs whose ids a wave reads once
 
 __device__ __forceinline__ int expert_of(const PlanArgs& a, int64_t p, int64_t end) {
@@ -326,6 +327,20 @@ __global__ __launch_bounds__(64 * kPlanWaves) void moe_place_kernel(PlanArgs a) 
   int held[kHeld];
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) held[i] = expert_of(a, begin + 64 * i + lane, end);
+  // a thread adds up one expert's counts over a part of the chunks, this one's
+  // and the later ones' apart
+  const int wide = min(E, (int)blockDim.x), parts = (int)blockDim.x / wide;
+  const int part = (int)threadIdx.x / wide, mine = (int)threadIdx.x - part * wide;
+  int sum = 0, sum_before = 0;
+  if (gridDim.x > 1 && part < parts) {
+    const int grid = (int)gridDim.x;
+#pragma unroll 8
+    for (int g = part; g < grid; g += parts) {
+      const int c = a.counts[(int64_t)g * E + mine];
+      sum += c;
+      sum_before += g < (int)blockIdx.x ? c : 0;
+    }
+  }
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
     total[e] = before[e] = 0;
 #pragma unroll
@@ -340,24 +355,9 @@ __global__ __launch_bounds__(64 * kPlanWaves) void moe_place_kernel(PlanArgs a) 
     const int e = expert_of(a, p, end);
     if (e >= 0) atomicAdd(&pos[wave][e], 1);
   }
-  if (gridDim.x > 1) {
-    // a thread adds up one expert's counts over a part of the chunks
-    const int grid = (int)gridDim.x;
-    for (int e0 = 0; e0 < E; e0 += blockDim.x) {
-      const int wide = min(E - e0, (int)blockDim.x), parts = (int)blockDim.x / wide;
-      const int part = (int)threadIdx.x / wide, e = e0 + (int)threadIdx.x - part * wide;
-      if (part < parts) {
-        int all = 0, mine = 0;
-#pragma unroll 8
-        for (int g = part; g < grid; g += parts) {
-          const int c = a.counts[(int64_t)g * E + e];
-          all += c;
-          mine += g < (int)blockIdx.x ? c : 0;
-        }
-        atomicAdd(&total[e], all);
-        atomicAdd(&before[e], mine);
-      }
-    }
+  if (gridDim.x > 1 && part < parts) {
+    atomicAdd(&total[mine], sum);
+    atomicAdd(&before[mine], sum_before);
   }
   __syncthreads();
   if (gridDim.x == 1) {
@@ -432,7 +432,10 @@ __global__ __launch_bounds__(64 * kPlanWaves) void moe_place_kernel(PlanArgs a) 
   for (int64_t e = tid; e <= E; e += step) a.offsets[e] = offset[e];
   if (tid < moe::kHeights) a.ntiles[tid] = first[tid][E];
   auto entry = [&](int h, int i, int e) {
-    reinterpret_cast<int4*>(a.tiles[h])[i] = make_int4(e, offset[e], offset[e + 1], first[h][e]);
+    int32_t* tiles = a.tiles[0];   // (selects: an indexed kernel argument would go through memory)
+#pragma unroll
+    for (int j = 1; j < moe::kHeights; ++j) tiles = h == j ? a.tiles[j] : tiles;
+    reinterpret_cast<int4*>(tiles)[i] = make_int4(e, offset[e], offset[e + 1], first[h][e]);
   };
   if (gridDim.x == 1 && most <= 8) {
     // few tiles each: a thread per expert and height writes them
@@ -441,18 +444,10 @@ __global__ __launch_bounds__(64 * kPlanWaves) void moe_place_kernel(PlanArgs a) 
       for (int k = first[h][e]; k < first[h][e + 1]; ++k) entry(h, k, e);
     }
   } else {
-#pragma unroll
-    for (int h = 0; h < moe::kHeights; ++h) {
-      const int n = first[h][E];
-      for (int64_t i = tid; i < n; i += step) {
-        int lo = 0, hi = E - 1;   // the last expert whose first tile is at most i: the one with tile i
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (first[h][mid] <= i) lo = mid;
-          else hi = mid - 1;
-        }
-        entry(h, (int)i, lo);
-      }
+    // a wave per expert and height
+    for (int i = blockIdx.x * kPlanWaves + wave; i < moe::kHeights * E; i += gridDim.x * kPlanWaves) {
+      const int h = i / E, e = i - h * E;
+      for (int k = first[h][e] + lane; k < first[h][e + 1]; k += 64) entry(h, k, e);
     }
   }
 }
@@ -556,7 +551,7 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(CombineArgs a) {
 
 hipError_t launch_moe_route(const RouteArgs& a, hipStream_t s) {
   const int e = a.experts;
-  if (a.tokens >= 2048 && e <= 256 && a.topk <= 16) {
+  if (a.tokens >= 6144 && e <= 256 && a.topk <= 16) {
     if (e <= 64) launch_route_nv<16, 4>(a, s);
     else if (e <= 128) launch_route_nv<16, 8>(a, s);
     else launch_route_nv<16, 16>(a, s);
