@@ -50,21 +50,27 @@ namespace mxfp4 {
 namespace large {
 
 // A workgroup's output tile: TBN weight rows x TBM activation rows on 2 x 2
-// waves, a ring of TNBUF stages, TWGS workgroups per CU.
-template <int TBN, int TBM, int TNBUF, int TWGS>
+// waves, a ring of TNBUF stages, TWGS workgroups per CU.  TTAIL: row-major
+// operands with K a multiple of 32 only.  The code blocks of the last stage past
+// K are read as zeros, from a constant of their own; scale bytes, at addresses of
+// any alignment, come one by one, a dword of LDS each.
+template <int TBN, int TBM, int TNBUF, int TWGS, bool TTAIL = false>
 struct Tile {
+  static constexpr bool TAIL = TTAIL;
   static constexpr int BN = TBN, BM = TBM, NBUF = TNBUF, WGS = TWGS;
   static constexpr int WN = 2, WM = 2, NW = WN * WM, NT = 64 * NW;
   static constexpr int ROWS = BN + BM;                        // rows per stage: W then X
   static constexpr int CODE_BYTES = ROWS * RB;
-  static constexpr int STAGE_BYTES = CODE_BYTES + ROWS * 4;
+  static constexpr int SCALE_BYTES = TAIL ? 16 : 4;           // per row
+  static constexpr int STAGE_BYTES = CODE_BYTES + ROWS * SCALE_BYTES;
   static constexpr int FN = BN / WN / 32, FM = BM / WM / 32;  // 32 x 32 fragments per wave
   // Per stage and wave: code loads of 1 KiB (16 rows), in stage row order, and
   // scale loads of 64 rows (the last one repeated where they do not divide).
   static constexpr int CODE_LOADS = ROWS / 16 / NW, SCALE_LOADS = (ROWS / 64 + NW - 1) / NW;
-  static constexpr int LPS = CODE_LOADS + SCALE_LOADS;
+  static constexpr int LPS = CODE_LOADS + SCALE_LOADS * (TAIL ? 4 : 1);
   static constexpr int CODE_LOADS_B = CODE_LOADS / 2;         // issued during sub-step 0
   static constexpr int NRD = FN + FM;                         // fragment reads per sub-step
+  static constexpr int NRS = NRD * (TAIL ? 2 : 1);            // scale reads per stage
   static constexpr bool WHOLE = BN % (16 * CODE_LOADS) == 0;  // no wave loads rows of both sides
   static_assert(ROWS % (16 * NW) == 0 && BN % 64 == 0, "whole loads per wave and side");
   static_assert(TWGS * TNBUF * STAGE_BYTES <= 160 * 1024, "LDS ring exceeds 160 KiB");
@@ -79,6 +85,11 @@ __device__ __forceinline__ void load_lds16(const uint8_t* src, uint8_t* dst) {
 __device__ __forceinline__ void load_lds4(const uint8_t* src, uint8_t* dst) {
   __builtin_amdgcn_global_load_lds(src, dst, 4, 0, 0);
 }
+// A byte per lane, each zero-extended to a dword of LDS.
+__device__ __forceinline__ void load_lds1(const uint8_t* src, uint8_t* dst) {
+  __builtin_amdgcn_global_load_lds(src, dst, 1, 0, 0);
+}
+__device__ const uint4 kZeroBlock = {0, 0, 0, 0};
 
 // Activation classes of the kernels that apply it in registers, to W values of a
 // fragment at a time.
@@ -228,7 +239,7 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(Args f,
   const int b = blockIdx.x;
   const int slot = xcd_remap ? (b & 7) * (grid >> 3) + (b >> 3) : b;
   if (slot >= ntiles) return;
-  const int nk = g.k / KS;
+  const int nk = T::TAIL ? (g.k + KS - 1) / KS : g.k / KS;
   const int total = ((ntiles - slot + grid - 1) / grid) * nk;
   const uint32_t kbytes = (uint32_t)g.k / 2, kblocks = (uint32_t)g.k / 32;
   const int lr = lane & 31, lg = lane >> 5;
@@ -359,15 +370,27 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(Args f,
   plan(0);
   auto issue_codes = [&](int i0, int i1) __attribute__((always_inline)) {
     uint8_t* dst = lds + ibuf * STAGE_BYTES;
+    // (TAIL: the lane's block of the stage is the same one in all its loads)
+    const bool in = !T::TAIL || 4 * ikt + ((lane & 3) ^ swz(lane >> 2)) < (int)kblocks;
 #pragma unroll
-    for (int i = i0; i < i1; ++i)
-      load_lds16(cbase[cb(i)] + ikt * cstride + coff[i], dst + code_group(i) * 1024);
+    for (int i = i0; i < i1; ++i) {
+      const uint8_t* src = cbase[cb(i)] + ikt * cstride + coff[i];
+      if constexpr (T::TAIL) src = in ? src : reinterpret_cast<const uint8_t*>(&kZeroBlock);
+      load_lds16(src, dst + code_group(i) * 1024);
+    }
   };
   auto issue_scales = [&]() __attribute__((always_inline)) {
     uint8_t* dst = lds + ibuf * STAGE_BYTES + CODE_BYTES;
 #pragma unroll
-    for (int i = 0; i < SCALE_LOADS; ++i)
-      load_lds4(sbase[i] + ikt * sstride + soff[i], dst + 256 * scale_group(i));
+    for (int i = 0; i < SCALE_LOADS; ++i) {
+      if constexpr (T::TAIL) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b)   // (past K the last block's again: their codes are zeros)
+          load_lds1(sbase[i] + min(4 * ikt + b, (int)kblocks - 1) + soff[i], dst + 4 * T::ROWS * b + 256 * scale_group(i));
+      } else {
+        load_lds4(sbase[i] + ikt * sstride + soff[i], dst + 256 * scale_group(i));
+      }
+    }
   };
   auto advance = [&]() __attribute__((always_inline)) {
     ibuf = ibuf + 1 == NBUF ? 0 : ibuf + 1;
@@ -384,12 +407,18 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(Args f,
 #pragma unroll
   for (int q = 0; q < FM; ++q) xrow[q] = BN + wm * (BM / WM) + 32 * q + lr;
   auto load_scales = [&](const uint8_t* sbuf, uint32_t (&sw)[FN], uint32_t (&sx)[FM]) {
+    auto two = [&](int row) -> uint32_t {   // scales of the lane's blocks of both sub-steps
+      if constexpr (T::TAIL) {
+        const uint8_t* p = sbuf + CODE_BYTES + 4 * row + 8 * T::ROWS * lg;
+        return *reinterpret_cast<const uint32_t*>(p) | *reinterpret_cast<const uint32_t*>(p + 4 * T::ROWS) << 8;
+      } else {
+        return *reinterpret_cast<const uint16_t*>(sbuf + CODE_BYTES + 4 * row + 2 * lg);
+      }
+    };
 #pragma unroll
-    for (int q = 0; q < FN; ++q)
-      sw[q] = *reinterpret_cast<const uint16_t*>(sbuf + CODE_BYTES + 4 * wrow[q] + 2 * lg);
+    for (int q = 0; q < FN; ++q) sw[q] = two(wrow[q]);
 #pragma unroll
-    for (int q = 0; q < FM; ++q)
-      sx[q] = *reinterpret_cast<const uint16_t*>(sbuf + CODE_BYTES + 4 * xrow[q] + 2 * lg);
+    for (int q = 0; q < FM; ++q) sx[q] = two(xrow[q]);
   };
   auto load_frags = [&](const uint8_t* sbuf, int s, u32x4 (&wf)[FN], u32x4 (&xf)[FM]) {
     const int c = 2 * lg + s;
@@ -506,7 +535,7 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(Args f,
       for (int a = 0; a < FN; ++a)
 #pragma unroll
         for (int c = 0; c < FM; ++c) acc[a][c] = mma<1>(wb[a], xb[c], acc[a][c], sw1[a], sx1[c]);
-      sched_substep<FN * FM, 2 * NRD, LPS - CODE_LOADS_B>();
+      sched_substep<FN * FM, NRD + T::NRS, LPS - CODE_LOADS_B>();
       __builtin_amdgcn_sched_barrier(0);
     }
 

@@ -131,8 +131,8 @@ hipError_t launch_residual_tiles(const FusedArgs& a, bool mid, hipStream_t s);  
 // plan (moe_plan.h) orders them, by weight e of a stack.  g.m rows in all; row p
 // of the result is that of plan row p.
 struct MoeArgs : FusedArgs {
-  const int32_t* tiles[5] = {};       // the plan's tile tables and their lengths
-  const int32_t* ntiles = nullptr;    // [5]
+  const int32_t* tiles[4] = {};       // the plan's tile tables and their lengths
+  const int32_t* ntiles = nullptr;    // [4]
   const int32_t* token = nullptr;     // row p reads row token[p] of A; null: row p
   int32_t a_rows = 0;                 // rows of A
   bool a_tiled = false;               // A's layout (g.tiled: the weights')
@@ -192,7 +192,7 @@ struct PlanArgs {
   const int32_t* ids;    // [pairs]
   int64_t pairs, chunk;
   int32_t topk, first, experts;
-  int32_t *offsets, *order, *slot, *token, *ntiles, *tiles[5], *counts;
+  int32_t *offsets, *order, *slot, *token, *ntiles, *tiles[4], *counts;
 };
 hipError_t launch_moe_plan(const PlanArgs& a, hipStream_t s);
 
@@ -213,8 +213,8 @@ struct CombineArgs {
 };
 hipError_t launch_moe_combine(const CombineArgs& a, hipStream_t s);
 
-// The kernel for the experts' products: row tiles of 16, 32 or 64 (small-M), 128
-// or 256 rows; 0: none.
+// The kernel for the experts' products: row tiles of 16 or 32 (small-M), 128 or
+// 256 rows.
 int moe_tile_rows(const MoeArgs& f);
 hipError_t launch_moe_small(const MoeArgs& f, int rows, hipStream_t s);
 hipError_t launch_moe_tiles(const MoeArgs& f, bool mid, hipStream_t s);

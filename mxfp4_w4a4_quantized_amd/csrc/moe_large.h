@@ -15,8 +15,11 @@ hipError_t launch_moe_tile(const MoeArgs& f, hipStream_t s) {
   return hipGetLastError();
 }
 
+typedef Tile<128, 128, 4, 2, true> MidTail;
+
 template <int ACT, int OUT, bool GLU>
 hipError_t launch_moe(const MoeArgs& f, bool mid, hipStream_t s) {
+  if (f.g.k % KS != 0) return launch_moe_tile<MidTail, ACT, OUT, GLU>(f, s);
   return mid ? launch_moe_tile<Mid, ACT, OUT, GLU>(f, s) : launch_moe_tile<Large, ACT, OUT, GLU>(f, s);
 }
 

@@ -18,11 +18,12 @@
 namespace mxfp4 {
 namespace moe {
 
-constexpr int kHeights = 5;                                  // 16, 32, 64, 128, 256 rows
+constexpr int kHeights = 4;                                  // rows of a tile: 16, 32, 128, 256
 constexpr int kMaxExperts = 1024;
 constexpr int64_t kMaxPairs = int64_t(1) << 28;
-constexpr int height_index(int rows) { return rows == 16 ? 0 : rows == 32 ? 1 : rows == 64 ? 2 : rows == 128 ? 3 : 4; }
-constexpr int64_t height(int i) { return int64_t(16) << i; }
+constexpr int shift_of(int i) { return i < 2 ? 4 + i : 5 + i; }   // height i is 2^this
+constexpr int height_index(int rows) { return rows == 16 ? 0 : rows == 32 ? 1 : rows == 128 ? 2 : 3; }
+constexpr int64_t height(int i) { return int64_t(1) << shift_of(i); }
 
 // Tiles of `rows` rows at most: a partial one per expert that has rows.
 inline int64_t max_tiles(int64_t pairs, int64_t experts, int64_t rows) {

@@ -372,7 +372,7 @@ __global__ __launch_bounds__(64 * kPlanWaves) void moe_place_kernel(PlanArgs a) 
   // wave 0: rows; wave 1 + h: tiles of height h
   if (wave <= moe::kHeights) {
     int32_t* out = wave == 0 ? offset : first[wave - 1];
-    const int shift = wave == 0 ? 0 : 3 + wave;   // 16 << h rows
+    const int shift = wave == 0 ? 0 : moe::shift_of(wave - 1);
     int carry = 0, top = 0;
     for (int e0 = 0; e0 < E; e0 += 64) {
       const int e = e0 + lane;

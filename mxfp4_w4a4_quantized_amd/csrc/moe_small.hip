@@ -1,5 +1,5 @@
 // The experts' products of few rows per expert (gemm_fused_small.h): row tiles of
-// 16, 32 or 64 rows, a workgroup per tile and 16 or 32 output columns.
+// 16 or 32 rows, a workgroup per tile and 16 or 32 output columns.
 #include "gemm_fused_small.h"
 
 namespace mxfp4 {
@@ -28,10 +28,9 @@ void launch(const MoeArgs& f, hipStream_t s) {
 
 template <int MG>
 void launch_mg(const MoeArgs& f, hipStream_t s) {
-  // Column groups of 16 of a dense output: two share an activation fragment (512
-  // tokens x 8 of 128 experts, 4096 -> 2 x 2048, row tiles of 32: 319 -> 259 us),
-  // where the accumulators leave registers for them.
-  constexpr int PG = MG <= 2 ? 2 : 1;
+  // Two column groups of 16 share an activation fragment (512 tokens x 8 of 128
+  // experts, 4096 -> 2 x 2048, row tiles of 32: 319 us with one, 259 with two).
+  constexpr int PG = 2;
   if (f.glu) {
     if (f.g.q_out) launch<MG, 2, 2, true>(f, s);
     else if (f.g.y_bf16) launch<MG, PG, 1, true>(f, s);
@@ -48,8 +47,7 @@ void launch_mg(const MoeArgs& f, hipStream_t s) {
 hipError_t launch_moe_small(const MoeArgs& f, int rows, hipStream_t s) {
   switch (rows) {
     case 16: launch_mg<1>(f, s); break;
-    case 32: launch_mg<2>(f, s); break;
-    default: launch_mg<4>(f, s); break;
+    default: launch_mg<2>(f, s); break;
   }
   return hipGetLastError();
 }

@@ -8,7 +8,7 @@ namespace mxfp4 {
 //    at 6 to 7.5 TB/s (64 tokens x 8 of 128 experts, 4096 -> 2 x 2048: 148 us in
 //    tiles of 16 rows, 191 in tiles of 128; 256 tokens 185 in 32, 208 in 128; 512
 //    tokens 259 in 32, 221 in 128).
-//  * Then the tile kernels where k allows them (64 rows otherwise), by fused_route's
+//  * Then the tile kernels, of 128 rows where k is no multiple of 128, by fused_route's
 //    model of their times on the tiles to expect, half a tile more for each expert
 //    than its rows fill (1024 tokens x 8 of 64 experts, 2048 -> 4096: 113 us in
 //    tiles of 128, 142 in 256; 1024 x 2 of 8 experts, 14336 -> 4096: 130 and 103).
@@ -19,7 +19,7 @@ int moe_tile_rows(const MoeArgs& f) {
   const int64_t mean = g.m / f.experts;
   if (mean <= 10) return 16;
   if (mean <= 20) return 32;
-  if (g.k % large::KS != 0) return 64;
+  if (g.k % large::KS != 0) return 128;
   const int64_t cus = cu_count(), nk = g.k / large::KS, wide = f.glu ? 2 * int64_t(g.n) : g.n;
   auto tiles = [&](int64_t t) { return (g.m / t + (f.experts + 1) / 2) * ((wide + t - 1) / t); };
   const int64_t t256 = tiles(256), t128 = tiles(128), rest = t128 % (2 * cus);

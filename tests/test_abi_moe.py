@@ -78,12 +78,12 @@ def test_plan_refusals():
 
 
 def test_plan_bytes_cover_every_table():
-    """Rows, slots, tokens, tiles of five heights and, past one chunk, its counts."""
+    """Rows, slots, tokens, tiles of four heights and, past one chunk, its counts."""
     for tokens, topk, experts in ((0, 1, 1), (1, 1, 1), (5, 3, 40), (4096, 1, 9), (4097, 1, 9), (100000, 7, 300)):
         p = tokens * topk
-        tiles = sum(p // (16 << i) + min(p, experts) for i in range(5))
+        tiles = sum(p // h + min(p, experts) for h in (16, 32, 128, 256))
         st, n = plan_bytes(tokens, topk, experts)
-        assert st == OK and n >= 4 * (experts + 1 + 3 * p + 5 + 4 * tiles)
+        assert st == OK and n >= 4 * (experts + 1 + 3 * p + 4 + 4 * tiles)
 
 
 def up_weights(**kw):

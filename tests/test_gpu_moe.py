@@ -121,11 +121,11 @@ def up64(a, wu, wg, bu, bg, act, tokens, experts):
     return h, b
 
 
-# (tokens, topk, experts, d, n): one pair; row tiles of 16, 32, 64, 128 and 256 rows
-# (by pairs / experts: up to 12, 24, 48, 512, more); K tails; odd widths
+# (tokens, topk, experts, d, n): one pair; row tiles of 16 and 32 rows (up to 10 and
+# 20 pairs an expert), of 128 and 256; K tails; odd widths
 UP = [(1, 1, 1, 128, 128), (1, 2, 8, 4096, 96), (5, 2, 3, 96, 40), (40, 3, 10, 160, 1000), (64, 4, 16, 512, 64),
       (61, 4, 12, 384, 300), (100, 3, 8, 1152, 33), (130, 2, 6, 96, 200), (300, 2, 5, 256, 300), (300, 2, 5, 128, 259),
-      (700, 3, 4, 640, 520), (1300, 1, 2, 256, 130), (1100, 2, 3, 1280, 515), (2600, 2, 3, 128, 258)]
+      (700, 3, 4, 640, 520), (1300, 1, 2, 256, 130), (1100, 2, 3, 1280, 515), (2600, 2, 3, 128, 258), (150, 2, 4, 32, 200), (400, 2, 3, 1184, 200), (1500, 2, 4, 416, 160)]
 
 
 @pytest.mark.parametrize("layout", [R, T])
@@ -214,7 +214,8 @@ def down64(h, wd, bias, weights, plan, residual):
 
 DOWN = [(1, 1, 1, 128, 128), (1, 2, 8, 1024, 96), (5, 3, 3, 96, 40), (40, 3, 10, 160, 1000), (64, 4, 16, 512, 64),
         (61, 4, 12, 384, 300), (100, 3, 8, 1152, 33), (300, 2, 5, 256, 300), (300, 2, 5, 128, 288), (700, 3, 4, 640, 520),
-        (700, 3, 4, 640, 544), (1100, 2, 3, 1280, 515), (2600, 2, 3, 128, 320)]
+        (700, 3, 4, 640, 544), (1100, 2, 3, 1280, 515), (2600, 2, 3, 128, 320),
+        (150, 2, 4, 64, 200), (400, 2, 3, 1184, 224), (1500, 2, 4, 416, 160)]
 
 
 @pytest.mark.parametrize("layout", [R, T])

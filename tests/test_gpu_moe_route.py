@@ -193,9 +193,8 @@ def check_plan(ids, experts, first=0, plan=None):
     at = experts + 1 + 2 * pairs
     assert np.array_equal(words[at:at + pairs], np.where(order >= 0, order // topk, 0))
     at = (at + pairs + 3) // 4 * 4
-    ntiles, at = words[at:at + 5], at + 8
-    for i in range(5):
-        h = 16 << i
+    ntiles, at = words[at:at + 4], at + 8
+    for i, h in enumerate((16, 32, 128, 256)):
         counts = np.diff(offsets)
         tiles = -(-counts // h)
         want = [(e, offsets[e], offsets[e + 1], tiles[:e].sum()) for e in range(experts) for _ in range(tiles[e])]
