@@ -630,10 +630,10 @@ typedef struct {
  *                     single products may be held in 16 bits, 11 of them
  *                     significant: an eighth of bf16's rounding
  *   workspace         device, 256-byte aligned, of mxfp4_moe_down_workspace bytes
- *                     (the products); needs no clearing, and calls that may
- *                     overlap in time need one each
- * Errors: as mxfp4_moe_up (a null weights or workspace, or a short one, is
- *   INVALID_ARG). */
+ *                     (the products; 0 for few pairs: then it may be NULL); needs
+ *                     no clearing, and calls that may overlap in time need one each
+ * Errors: as mxfp4_moe_up (null weights are INVALID_ARG, and so is a workspace
+ *   that is missing or too short). */
 MXFP4_API mxfp4_status mxfp4_moe_down_workspace(int64_t tokens, int64_t topk, int64_t experts, int64_t n, int64_t k,
                                                 int32_t layout, int32_t y_dtype, int64_t* bytes);
 MXFP4_API mxfp4_status mxfp4_moe_down(const uint8_t* h_codes, const uint8_t* h_scales, const void* plan,

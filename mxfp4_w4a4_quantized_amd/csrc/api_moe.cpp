@@ -240,7 +240,7 @@ MXFP4_API mxfp4_status mxfp4_moe_down_workspace(int64_t tokens, int64_t topk, in
   f.g.k = static_cast<int32_t>(k);
   f.experts = static_cast<int32_t>(experts);
   const int height = mxfp4::moe_tile_rows(f);
-  *bytes = tokens == 0 || n == 0 ? 0 : product_bytes(tokens * topk, n, half_products(f, height, y_dtype));
+  *bytes = tokens == 0 || n == 0 || mxfp4::moe_down_small(f) ? 0 : product_bytes(tokens * topk, n, half_products(f, height, y_dtype));
   return MXFP4_OK;
 }
 
@@ -267,20 +267,7 @@ MXFP4_API mxfp4_status mxfp4_moe_down(const uint8_t* h_codes, const uint8_t* h_s
   if (st != MXFP4_OK) return st;
   f.vec_bf16 = w->vec_dtype == MXFP4_BF16;
   f.bias = w->bias;
-  const bool half = half_products(f, height, y_dtype);
-  if (workspace == nullptr || workspace_bytes < product_bytes(pairs, n, half)) return MXFP4_ERR_INVALID_ARG;
-  if (!aligned(workspace, 256)) return MXFP4_ERR_UNSUPPORTED;
-  f.g.y = workspace;
-  f.g.ld_y = n;
-  f.g.y_bf16 = false;
-  f.z_half = half;
-  f.z_scales = half ? static_cast<uint8_t*>(workspace) + (pairs * n * 2 + 255) / 256 * 256 : nullptr;
-  st = launch(f, height, stream);
-  if (st != MXFP4_OK) return st;
   mxfp4::CombineArgs c{};
-  c.z = workspace;
-  c.z_scales = f.z_scales;
-  c.half = half;
   c.slot = static_cast<const int32_t*>(plan) + mxfp4::moe::plan_layout(pairs, experts).slot;
   c.weights = weights;
   c.residual = residual;
@@ -292,6 +279,20 @@ MXFP4_API mxfp4_status mxfp4_moe_down(const uint8_t* h_codes, const uint8_t* h_s
   c.tokens = tokens;
   c.topk = static_cast<int32_t>(topk);
   c.n = static_cast<int32_t>(n);
+  if (mxfp4::moe_down_small(f)) return from_hip(mxfp4::launch_moe_down_small(f, c, static_cast<hipStream_t>(stream)));
+  const bool half = half_products(f, height, y_dtype);
+  if (workspace == nullptr || workspace_bytes < product_bytes(pairs, n, half)) return MXFP4_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256)) return MXFP4_ERR_UNSUPPORTED;
+  f.g.y = workspace;
+  f.g.ld_y = n;
+  f.g.y_bf16 = false;
+  f.z_half = half;
+  f.z_scales = half ? static_cast<uint8_t*>(workspace) + (pairs * n * 2 + 255) / 256 * 256 : nullptr;
+  c.z = workspace;
+  c.z_scales = f.z_scales;
+  c.half = half;
+  st = launch(f, height, stream);
+  if (st != MXFP4_OK) return st;
   return from_hip(mxfp4::launch_moe_combine(c, static_cast<hipStream_t>(stream)));
 }
 

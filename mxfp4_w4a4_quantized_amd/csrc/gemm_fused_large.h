@@ -500,7 +500,26 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(Args f,
     // wait states before the K loop's MFMAs read them
     mfma_wait();
 
-    for (int kt = 0; kt < nk; ++kt) {
+    // MOE: a wave without rows in the tile (an expert's last) only keeps the ring
+    // going.  (A loop of its own: a branch in the other one would hold up its MFMAs.)
+    int k0 = 0;
+    if constexpr (MOE) {
+      if (at.row0 + wm * (BM / WM) >= end) {
+        for (; k0 < nk; ++k0) {
+          advance();
+          wait_stages<NBUF - 3, LPS>();
+          __builtin_amdgcn_s_barrier();
+          __builtin_amdgcn_sched_barrier(0);
+          cbuf = cbuf + 1 == NBUF ? 0 : cbuf + 1;
+          issue_codes(0, CODE_LOADS);
+          issue_scales();
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        load_scales(lds + cbuf * STAGE_BYTES, sw, sx);
+        load_frags(lds + cbuf * STAGE_BYTES, 0, wa, xa);
+      }
+    }
+    for (int kt = k0; kt < nk; ++kt) {
       if constexpr (AHEAD) {
         if (kt == ahead) prefetch_res(at.row0, tn);
       }
@@ -746,6 +765,8 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(Args f,
         if constexpr (PIECES) {
           if (f.residual != nullptr && p + RD - 1 < NP) load_res(p + RD - 1);
         }
+        uint32_t zbytes = 0;
+        static_assert(OUT != 3 || FPP == 4 || FPP == 2, "z scale bytes of a pass");
 #pragma unroll
         for (int o = o0; o < o0 + FPP; ++o) {
           float v[16];
@@ -763,9 +784,20 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(Args f,
             const float sc = __uint_as_float((268u - ef) << 23);                   // 2^(14 - (ef - 127))
 #pragma unroll
             for (int r = 0; r < 16; ++r) v[r] = v[r] * sc;
+            // a row's bytes of the pass together where they are aligned: a store of
+            // single bytes costs as much as one of whole lines
             const int m = mw0 + 32 * bb + lr, n = nw0 + 32 * o;
-            if (lg == 0 && m < end && n < g.n)
-              f.z_scales[(int64_t)m * (g.n >> 5) + (n >> 5)] = (uint8_t)(ef - 14u);
+            uint8_t* zs = f.z_scales + (int64_t)m * (g.n >> 5) + (n >> 5);
+            const bool ok = lg == 0 && m < end && n < g.n;
+            if (g.n % (32 * FPP) != 0) {
+              if (ok) *zs = (uint8_t)(ef - 14u);
+            } else {
+              zbytes = o == o0 ? ef - 14u : zbytes | (ef - 14u) << (8 * (o - o0));
+              if (o == o0 + FPP - 1 && ok) {
+                if constexpr (FPP == 4) *reinterpret_cast<uint32_t*>(zs - 3) = zbytes;
+                else *reinterpret_cast<uint16_t*>(zs - 1) = (uint16_t)zbytes;
+              }
+            }
           }
 #pragma unroll
           for (int t = 0; t < 4; ++t) {

@@ -218,5 +218,8 @@ hipError_t launch_moe_combine(const CombineArgs& a, hipStream_t s);
 int moe_tile_rows(const MoeArgs& f);
 hipError_t launch_moe_small(const MoeArgs& f, int rows, hipStream_t s);
 hipError_t launch_moe_tiles(const MoeArgs& f, bool mid, hipStream_t s);
+// The down projection and the weighted sum in one kernel, and whether it is the one.
+bool moe_down_small(const MoeArgs& f);
+hipError_t launch_moe_down_small(const MoeArgs& f, const CombineArgs& c, hipStream_t s);
 
 }  // namespace mxfp4
