@@ -19,9 +19,10 @@ namespace {
 //
 // G lanes serve a token, expert G i + lane of them in register i.  64 lanes give
 // the shortest time for few tokens; for many, 16 lanes: of the instructions of a
-// choice those between lanes are then shared by four tokens (8192 tokens x 256
-// experts, sigmoid, bias, groups: @ROUTE@).  What remains is the 64-bit arithmetic
-// of an exponential and a reciprocal for each score.
+// choice those between lanes are then shared by four tokens.  Bound by launch and
+// load latency for few tokens (16 x 128, topk 8: 4.0 us; 2.9 of them with topk 1),
+// by 64-bit arithmetic for many (8192 x 256, topk 8: softmax 9.2 us; sigmoid, bias
+// and 8 groups 16.6, of them 4 the scores, 3 the groups, 3 the choice).
 
 // Below every key: none is left.  Keys are kept within +-1e308.
 constexpr uint32_t kNoneHigh = 0xFFEFFFFFu;   // of -1.79e308
@@ -63,6 +64,32 @@ __device__ __forceinline__ double rotated(double v) {
 template <int CTRL>
 __device__ __forceinline__ float rotated(float v) { return __uint_as_float(rotated<CTRL>(__float_as_uint(v))); }
 
+// v of the rows (16 lanes) or the halves of the wave, paired: of each pair both
+// values in both lanes.
+template <int ROWS>
+__device__ __forceinline__ void paired(uint32_t v, uint32_t& a, uint32_t& b) {
+  const auto r = ROWS == 1 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
+                           : __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  a = r[0];
+  b = r[1];
+}
+template <int ROWS>
+__device__ __forceinline__ void paired(float v, float& a, float& b) {
+  uint32_t x, y;
+  paired<ROWS>(__float_as_uint(v), x, y);
+  a = __uint_as_float(x);
+  b = __uint_as_float(y);
+}
+template <int ROWS>
+__device__ __forceinline__ void paired(double v, double& a, double& b) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  uint32_t xl, yl, xh, yh;
+  paired<ROWS>((uint32_t)u, xl, yl);
+  paired<ROWS>((uint32_t)(u >> 32), xh, yh);
+  a = __builtin_bit_cast(double, ((uint64_t)xh << 32) | xl);
+  b = __builtin_bit_cast(double, ((uint64_t)yh << 32) | yl);
+}
+
 struct Max {
   template <typename T> __device__ __forceinline__ T operator()(T a, T b) const { return larger(a, b); }
 };
@@ -79,40 +106,56 @@ __device__ __forceinline__ T across(T v, Op op) {
   v = op(v, rotated<0x122>(v));
   v = op(v, rotated<0x121>(v));
   if constexpr (G == 64) {
-    v = op(__shfl_xor(v, 16), v);
-    v = op(__shfl_xor(v, 32), v);
+    T a, b;
+    paired<1>(v, a, b);
+    paired<2>(op(a, b), a, b);
+    v = op(a, b);
   }
   return v;
 }
 
 // e^x in 64 bits, relative error some 2^-47: x = n ln 2 + r, |r| <= ln 2 / 2, with
 // ln 2 in two parts (Cody and Waite), and the series of e^r to r^11.  0 below -700.
-__device__ __forceinline__ double exp64(double x) {
-  const double n = __builtin_rint(x * 1.4426950408889634);
-  const double r = __builtin_fma(n, -1.9082149292705877e-10, __builtin_fma(n, -0.69314718036912382, x));
-  double p = 1.0 / 39916800;
-  p = __builtin_fma(p, r, 1.0 / 3628800);
-  p = __builtin_fma(p, r, 1.0 / 362880);
-  p = __builtin_fma(p, r, 1.0 / 40320);
-  p = __builtin_fma(p, r, 1.0 / 5040);
-  p = __builtin_fma(p, r, 1.0 / 720);
-  p = __builtin_fma(p, r, 1.0 / 120);
-  p = __builtin_fma(p, r, 1.0 / 24);
-  p = __builtin_fma(p, r, 1.0 / 6);
-  p = __builtin_fma(p, r, 0.5);
-  p = __builtin_fma(p, r, 1.0);
-  p = __builtin_fma(p, r, 1.0);
-  return x < -700.0 ? 0.0 : __builtin_ldexp(p, (int)n);
+// N values step by step together: one alone waits for each of its operations.
+template <int N>
+__device__ __forceinline__ void exp64(double (&x)[N]) {
+  constexpr double kSeries[] = {1.0 / 39916800, 1.0 / 3628800, 1.0 / 362880, 1.0 / 40320, 1.0 / 5040, 1.0 / 720,
+                                1.0 / 120,      1.0 / 24,      1.0 / 6,      0.5,         1.0,        1.0};
+  double big[N], r[N], p[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) big[i] = __builtin_fma(x[i], 1.4426950408889634, 0x1.8p52);   // n in its lowest bits
+#pragma unroll
+  for (int i = 0; i < N; ++i) r[i] = __builtin_fma(big[i] - 0x1.8p52, -0.69314718036912382, x[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) r[i] = __builtin_fma(big[i] - 0x1.8p52, -1.9082149292705877e-10, r[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) p[i] = kSeries[0];
+#pragma unroll
+  for (int t = 1; t < 12; ++t) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = __builtin_fma(p[i], r[i], kSeries[t]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {   // p 2^n by its exponent field
+    const uint64_t e = __builtin_bit_cast(uint64_t, p[i]) + (__builtin_bit_cast(uint64_t, big[i]) << 52);
+    x[i] = x[i] < -700.0 ? 0.0 : __builtin_bit_cast(double, e);
+  }
 }
-// 1 / x by two Newton steps on the instruction's 2^-14 or better (x normal).
-__device__ __forceinline__ double rcp64(double x) {
-  double r = __builtin_amdgcn_rcp(x);
-  r = __builtin_fma(__builtin_fma(-x, r, 1.0), r, r);
-  return __builtin_fma(__builtin_fma(-x, r, 1.0), r, r);
-}
-__device__ __forceinline__ double sigmoid64(double x) {
-  const double e = exp64(-__builtin_fabs(x)), r = rcp64(1.0 + e);
-  return x < 0.0 ? e * r : r;
+// 1 / (1 + e^-x).  v_rcp_f64 is right to some 2^-23, a Newton step makes that 2^-45,
+// beyond what a key keeps.
+template <int N>
+__device__ __forceinline__ void sigmoid64(double (&x)[N]) {
+  double e[N], r[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) e[i] = -__builtin_fabs(x[i]);
+  exp64(e);
+#pragma unroll
+  for (int i = 0; i < N; ++i) r[i] = __builtin_amdgcn_rcp(1.0 + e[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) r[i] = __builtin_fma(__builtin_fma(-(1.0 + e[i]), r[i], 1.0), r[i], r[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = x[i] < 0.0 ? e[i] * r[i] : r[i];
 }
 
 constexpr int kRouteWaves = 4;
@@ -150,14 +193,20 @@ __global__ __launch_bounds__(64 * kRouteWaves) void moe_route_kernel(RouteArgs a
   double s[ALL ? NV : 1], scale = 1.0;
   if (ALL || (a.softmax && !a.renormalize)) {
     double sum = 0.0;
+    constexpr int N = NV < 4 ? NV : 4;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      double v = 0.0;
-      if (a.softmax) v = exp64((double)x[i] - (double)top);
-      else if constexpr (ALL) v = sigmoid64((double)x[i]);
-      v = x[i] > -kInf ? v : 0.0;
-      sum += v;
-      if constexpr (ALL) s[i] = v;
+    for (int i0 = 0; i0 < NV; i0 += N) {
+      double v[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = a.softmax ? (double)x[i0 + i] - (double)top : (double)x[i0 + i];
+      if (a.softmax) exp64(v);
+      else if constexpr (ALL) sigmoid64(v);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        v[i] = x[i0 + i] > -kInf ? v[i] : 0.0;
+        sum += v[i];
+        if constexpr (ALL) s[i0 + i] = v[i];
+      }
     }
     if (a.softmax) scale = 1.0 / across<G>(sum, Sum());
   }
@@ -230,18 +279,26 @@ __global__ __launch_bounds__(64 * kRouteWaves) void moe_route_kernel(RouteArgs a
 #pragma unroll
     for (int i = 1; i < NV; ++i) best = larger(best, key[i]);
     best = across<G>(best, Max());
-    const uint64_t b = __builtin_bit_cast(uint64_t, best);
+    const int e = key_index(best), mine = e - sub;   // this lane's register e / G, if it has it
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
+    for (int i = 0; i < NV; ++i) {   // (the upper half alone makes it none)
       const uint64_t u = __builtin_bit_cast(uint64_t, key[i]);
-      key[i] = u == b ? none() : key[i];
+      const uint32_t high = mine == G * i ? kNoneHigh : (uint32_t)(u >> 32);
+      key[i] = __builtin_bit_cast(double, ((uint64_t)high << 32) | (uint32_t)u);
     }
-    if (sub == j) id = is_none(best) ? -1 : key_index(best);
+    if (sub == j) id = is_none(best) ? -1 : e;
   }
   double w = 0.0;
   if (id >= 0) {
-    const double l = (double)logit(id);
-    w = a.softmax ? exp64(l - (double)top) * scale : sigmoid64(l);
+    double l[1] = {(double)logit(id)};
+    if (a.softmax) {
+      l[0] -= (double)top;
+      exp64(l);
+      w = l[0] * scale;
+    } else {
+      sigmoid64(l);
+      w = l[0];
+    }
   }
   if (a.renormalize) {
     const double sum = across<G>(w, Sum());
