@@ -530,8 +530,9 @@ typedef enum {
  * group scores are formed in binary64 (two s + bias that agree to 2^-42 of their
  * value count as equal), weights rounded once.
  * Logits of -infinity or NaN are experts that cannot be chosen; a bias of
- * -infinity takes one out as well.  Where fewer than topk can be chosen, the
- * remaining ids are -1 with weight 0. */
+ * -infinity or NaN takes one out as well.  Where fewer than topk can be chosen,
+ * the remaining ids are -1 with weight 0.  A logit of +infinity makes a token's
+ * softmax NaN: its weights are, and with a bias none of its experts is chosen. */
 typedef struct {
     int32_t score;         /* mxfp4_score */
     int32_t topk;          /* 1 .. experts */

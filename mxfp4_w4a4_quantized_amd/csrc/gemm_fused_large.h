@@ -777,6 +777,12 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(Args f,
             float am = 0.0f;
 #pragma unroll
             for (int r = 0; r < 16; ++r) am = fmaxf(am, fabsf(v[r]));
+            // (an infinity stays one at any scale: the largest finite value counts)
+            if (__builtin_expect(__builtin_amdgcn_ballot_w64(am == __builtin_inff()) != 0, 0)) {
+              am = 0.0f;
+#pragma unroll
+              for (int r = 0; r < 16; ++r) am = fabsf(v[r]) < __builtin_inff() ? fmaxf(am, fabsf(v[r])) : am;
+            }
             float other = am;
             swap_halves(am, other);
             am = fmaxf(am, other);

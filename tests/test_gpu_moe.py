@@ -309,6 +309,79 @@ def test_down_far_scales(e):
     check(y[:, torch.from_numpy(keep)], want[:, keep], bound[:, keep], "beside NaN")
 
 
+def test_down_infinite_products():
+    """A product that leaves fp32's range reaches its own element only, in the
+    16-bit form too."""
+    rng = np.random.default_rng(11)
+    tokens, topk, experts, k, n = 300, 2, 2, 128, 256
+    c, s = workloads.random_mxfp4(rng, tokens * topk, k, -6, -4)
+    h = oracle.dequantize(c, s)
+    w = [workloads.random_mxfp4(rng, n, k, -1, 1) for _ in range(experts)]
+    wd = [oracle.dequantize(*x) for x in w]
+    for x in w:                                       # column 70: products of some 2^127 and more
+        x[1][70] = 254
+    col = [oracle.dequantize(*x)[70] for x in w]
+    tw = [mx.tile_host(*x) for x in w]
+    wdd = (to_dev(np.stack([x[0] for x in tw])), to_dev(np.stack([x[1] for x in tw])))
+    c, s = (to_dev(t) for t in mx.tile_host(c, s))
+    plan = mx.moe_plan(to_dev(rng.integers(0, experts, (tokens, topk)).astype(np.int32)), experts)
+    weights = torch.ones(tokens, topk, device=DEV)
+    want, S, Z = down64(h, wd, None, weights.double().cpu().numpy(), plan, None)
+    announce("moe_down, infinities")
+    y = mx.moe_down(c, s, plan, weights, wdd, layout=T)
+    keep = np.arange(n) != 70
+    other = (torch.arange(n) // 32 == 70 // 32).numpy()
+    assert torch.isinf(y[:, 70].float()).any()
+    near = keep & other                                # the block's other columns: held beside numbers of 2^127
+    far = keep & ~other
+    check(y[:, torch.from_numpy(far)], want[:, far], ((topk + 2) * U * S + 2.0 ** -11 * S + 2.0 ** -24 * Z)[:, far], "other blocks")
+    both = np.ones(tokens, bool)                       # tokens whose every product in column 70 is infinite
+    order, ex = rows_of(plan)
+    z = np.array([h[p] @ col[e] for p, e in enumerate(ex)])
+    np.logical_and.at(both, order // topk, np.abs(z) > 3.5e38)
+    assert both.any()
+    sel = np.ix_(both, near)
+    check(y[torch.from_numpy(both)][:, torch.from_numpy(near)], want[sel], ((topk + 2) * U * S + 2.0 ** -11 * S + 2.0 ** -24 * Z)[sel],
+          "beside infinities")
+
+
+def test_rows_past_4_gib():
+    """Results and products whose byte offsets pass 32 bits, on a sample of rows."""
+    rng = np.random.default_rng(12)
+    tokens, topk, experts, k, n = 36000, 8, 24, 128, 4096
+    a, ac, as_ = operand(rng, tokens, k, -6, -4, T)
+    w, wd = experts_weights(rng, experts, n, k, T)
+    ids = np.stack([rng.permutation(experts)[:topk] for _ in range(tokens)]).astype(np.int32)
+    plan = mx.moe_plan(to_dev(ids), experts)
+    pairs, ex = rows_of(plan)
+    some = np.unique(np.concatenate(([0, 1, len(pairs) - 1, len(pairs) - 2], rng.integers(0, len(pairs), 60),
+                                     rng.integers(2 ** 32 // (4 * n), len(pairs), 60))))
+    want = np.stack([w[ex[p]] @ a[pairs[p] // topk] for p in some])
+    for out in (F, BF):
+        announce("moe_up past 4 GiB", out)
+        y = mx.moe_up(ac, as_, plan, wd, act="none", out_dtype=out, layout=T, n=n)
+        assert y.numel() * y.element_size() > (2 ** 32 if out == F else 2 ** 31)
+        check(y[torch.from_numpy(some).to(DEV)], want, 0 * want, str(out))
+        del y
+    hc, hs = workloads.random_mxfp4(rng, tokens * topk, k, -6, -4)
+    slot = plan.slot.cpu().numpy().reshape(tokens, topk)
+    some = np.unique(np.concatenate(([0, tokens - 1], rng.integers(0, tokens, 40))))
+    weights = torch.rand(tokens, topk, device=DEV)
+    want, S, Z = np.zeros((len(some), n)), np.zeros((len(some), n)), np.zeros((len(some), n))
+    for i, t in enumerate(some):
+        for j in range(topk):
+            z = w[ids[t, j]] @ oracle.dequantize(hc[slot[t, j]][None], hs[slot[t, j]][None])[0]
+            q = float(weights[t, j])
+            want[i] += q * z
+            S[i] += np.abs(q * z)
+            Z[i] += q * np.abs(z).reshape(-1, 32).max(1).repeat(32)
+    tc, ts = (to_dev(x) for x in mx.tile_host(hc, hs))
+    for out in (F, BF):
+        announce("moe_down past 4 GiB", out)
+        y = mx.moe_down(tc, ts, plan, weights, wd, out_dtype=out, layout=T, n=n)
+        check(y[torch.from_numpy(some).to(DEV)], want, (topk + 2) * U * S + (2.0 ** -11 * S + 2.0 ** -24 * Z if out == BF else 0), str(out))
+
+
 # ---------------------------------------------------------------------------
 # the block
 
