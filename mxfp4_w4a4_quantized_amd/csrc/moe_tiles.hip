@@ -4,10 +4,11 @@
 namespace mxfp4 {
 
 // The height of the row tiles, by the mean number of rows of an expert.
-//  * Up to 10 rows 16, up to 20 rows 32: the weights are streamed once or nearly,
-//    at 6 to 7.5 TB/s (64 tokens x 8 of 128 experts, 4096 -> 2 x 2048: 148 us in
-//    tiles of 16 rows, 191 in tiles of 128; 256 tokens 185 in 32, 208 in 128; 512
-//    tokens 259 in 32, 221 in 128).
+//  * Up to 7 rows 16, up to 18 rows 32: the weights are streamed once or nearly, at 6
+//    to 7.5 TB/s (8 of 128 experts, 4096 -> 2 x 2048, gated; us in tiles of 16, 32 and
+//    128 rows: mean 6 161, 171, 193; 8 169, 166, 189; 12 199, 179, 197; 20 269, 218,
+//    210).  From k = 8192 on up to 10 rows: there the tile kernel's stream is the
+//    faster one (2 of 8 experts, 14336 -> 4096: mean 12 57 in 32, 43 in 128).
 //  * Then the tile kernels, of 128 rows where k is no multiple of 128, by fused_route's
 //    model of their times on the tiles to expect, half a tile more for each expert
 //    than its rows fill (1024 tokens x 8 of 64 experts, 2048 -> 4096: 113 us in
@@ -17,8 +18,8 @@ namespace mxfp4 {
 int moe_tile_rows(const MoeArgs& f) {
   const GemmArgs& g = f.g;
   const int64_t mean = g.m / f.experts;
-  if (mean <= 10) return 16;
-  if (mean <= 20) return 32;
+  if (mean <= 7) return 16;
+  if (mean <= (g.k >= 8192 ? 10 : 18)) return 32;
   if (g.k % large::KS != 0) return 128;
   const int64_t cus = cu_count(), nk = g.k / large::KS, wide = f.glu ? 2 * int64_t(g.n) : g.n;
   auto tiles = [&](int64_t t) { return (g.m / t + (f.experts + 1) / 2) * ((wide + t - 1) / t); };

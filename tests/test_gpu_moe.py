@@ -121,8 +121,8 @@ def up64(a, wu, wg, bu, bg, act, tokens, experts):
     return h, b
 
 
-# (tokens, topk, experts, d, n): one pair; row tiles of 16 and 32 rows (up to 10 and
-# 20 pairs an expert), of 128 and 256; K tails; odd widths
+# (tokens, topk, experts, d, n): one pair; row tiles of 16 and 32 rows (up to 7 and 18
+# pairs an expert) and of 128; K tails; odd widths
 UP = [(1, 1, 1, 128, 128), (1, 2, 8, 4096, 96), (5, 2, 3, 96, 40), (40, 3, 10, 160, 1000), (64, 4, 16, 512, 64),
       (61, 4, 12, 384, 300), (100, 3, 8, 1152, 33), (130, 2, 6, 96, 200), (300, 2, 5, 256, 300), (300, 2, 5, 128, 259),
       (700, 3, 4, 640, 520), (1300, 1, 2, 256, 130), (1100, 2, 3, 1280, 515), (2600, 2, 3, 128, 258), (150, 2, 4, 32, 200), (400, 2, 3, 1184, 200), (1500, 2, 4, 416, 160)]
@@ -173,6 +173,66 @@ def test_up(tokens, topk, experts, d, n, gated, layout):
                 else:
                     hc, hs = yc[:len(pairs)].cpu().numpy(), ys[:len(pairs)].cpu().numpy()
                 assert np.array_equal(hc, qc.cpu().numpy()) and np.array_equal(hs, qs.cpu().numpy())
+
+
+# Several tiles a workgroup: of 128 rows, with K of one stage (the ring is then three
+# tiles ahead), two and three; of 256 rows.
+LARGE = [(3000, 2, 4, 128, 8200), (1500, 3, 3, 256, 8200), (1000, 3, 3, 384, 8200), (3000, 2, 2, 768, 12900),
+         (1500, 3, 3, 1024, 9000), (2100, 2, 5, 1280, 12900)]
+
+
+@pytest.mark.parametrize("gated", [True, False])
+@pytest.mark.parametrize("tokens,topk,experts,d,n", LARGE)
+def test_large_tiles(tokens, topk, experts, d, n, gated):
+    """A sample of rows, the last and first ones of the experts among them; each of
+    all columns.  moe_up in fp32, bf16 and MXFP4, moe_down (not gated) in both."""
+    rng = np.random.default_rng(tokens)
+    n //= 2 if gated else 1
+    n8 = n // 128 * 128
+    a, ac, as_ = operand(rng, tokens, d, -6, -4, T)
+    wu, wud = experts_weights(rng, experts, n8, d, T)
+    wg, wgd = experts_weights(rng, experts, n8, d, T) if gated else (None, None)
+    ids = choose(rng, tokens, topk, experts, "part")
+    plan = mx.moe_plan(to_dev(ids.astype(np.int32)), experts)
+    pairs, ex = rows_of(plan)
+    edges = plan.offsets.cpu().numpy()
+    some = np.unique(np.clip(np.concatenate((edges, edges - 1, edges + 255, edges + 256, rng.integers(0, len(pairs), 200))), 0,
+                             len(pairs) - 1))
+    bu = to_dev(rng.standard_normal((experts, n8)).astype(np.float32))
+    want, bound = up64(a, wu, wg, bu.double().cpu().numpy(), None, "silu", pairs[some] // topk, ex[some])
+    at = torch.from_numpy(some).to(DEV)
+    kw = dict(w_gate=wgd, act="silu", bias_up=bu, layout=T, n=n8)
+    for out in (F, BF):
+        announce("moe_up, large tiles", tokens, topk, experts, d, n8, gated, out)
+        y = mx.moe_up(ac, as_, plan, wud, out_dtype=out, **kw)
+        check(y[at], want, bound, str(out))
+        if out == F:
+            exact = y[:len(pairs)].clone()
+    yc, ys = mx.moe_up_requant(ac, as_, plan, wud, rot="h32", out_layout=T, **kw)
+    qc, qs = mx.quantize_rotate(exact, "h32", layout=T)
+    # whole 256-row tiles of the layout
+    rows = len(pairs) // 256 * 256
+    assert torch.equal(yc[:rows], qc[:rows]) and torch.equal(ys[:rows], qs[:rows])
+    if gated:
+        return
+    h, hc, hs = operand(rng, tokens * topk, d, -6, -4, T)
+    weights = torch.rand(tokens, topk, device=DEV)
+    residual = torch.randn(tokens, n8, device=DEV)
+    slot = plan.slot.cpu().numpy().reshape(tokens, topk)
+    some = np.unique(np.concatenate(([0, tokens - 1, tokens // 2], rng.integers(0, tokens, 100))))
+    want = residual[torch.from_numpy(some).to(DEV)].double().cpu().numpy()
+    S, Z = np.abs(want), 0 * want
+    for i, t in enumerate(some):
+        for j in range(topk):
+            if slot[t, j] >= 0:
+                q, z = float(weights[t, j]), wu[ids[t, j]] @ h[slot[t, j]] + bu[ids[t, j]].double().cpu().numpy()
+                want[i] += q * z
+                S[i] += np.abs(q * z)
+                Z[i] += q * np.abs(z).reshape(-1, 32).max(1).repeat(32)
+    for out in (F, BF):
+        announce("moe_down, large tiles", out)
+        y = mx.moe_down(hc, hs, plan, weights, wud, bias=bu, residual=residual, out_dtype=out, layout=T, n=n8)
+        check(y[torch.from_numpy(some).to(DEV)], want, (topk + 2) * U * S + (2.0 ** -11 * S + 2.0 ** -24 * Z if out == BF else 0), str(out))
 
 
 def test_up_requant_leaves_rows_behind_the_last():
