@@ -2,6 +2,9 @@
 // and the plan that puts the (token, choice) pairs in expert order.
 #include "internal.h"
 #include "moe_plan.h"
+#include "moe_tile.h"
+
+#include <type_traits>
 
 namespace mxfp4 {
 namespace {
@@ -514,6 +517,8 @@ __global__ __launch_bounds__(64 * kPlanWaves) void moe_place_kernel(PlanArgs a) 
 // in 16 bits with a power of two per 32 columns; fp32 sums in the choices' order,
 // rounded once.  A lane holds 8 columns of a row.
 
+constexpr int kAhead = 8;
+
 template <bool HALF, bool VEC>
 __global__ __launch_bounds__(256) void moe_combine_kernel(CombineArgs a) {
   const int64_t t = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
@@ -548,32 +553,44 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(CombineArgs a) {
       }
     }
   }
+  // Slots and weights are the same for the whole workgroup (scalar loads); kAhead
+  // rows are asked for together.
   const int32_t* slot = a.slot + t * a.topk;
-  const float* weight = a.weights + t * a.topk;
-#pragma unroll 4
-  for (int j = 0; j < a.topk; ++j) {
-    const int row = slot[j];
-    const bool here = row >= 0;   // (else z's first row is read and not used)
-    const float w = weight[j];
-    const int64_t at = (int64_t)max(row, 0) * a.n + n0;
-    if constexpr (HALF) {
-      typedef _Float16 h8 __attribute__((ext_vector_type(8)));
-      const h8 z = *reinterpret_cast<const h8*>(static_cast<const _Float16*>(a.z) + at);
-      const float f = __uint_as_float((uint32_t)a.z_scales[at >> 5] << 23);   // (never 0: see the product's epilogue)
+  const int32_t* weight = reinterpret_cast<const int32_t*>(a.weights + t * a.topk);
+  typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+  typedef float f8 __attribute__((ext_vector_type(8)));
+  typedef std::conditional_t<HALF, h8, f8> Row;
+  for (int j0 = 0; j0 < a.topk; j0 += kAhead) {
+    Row z[kAhead];
+    uint32_t scale[kAhead];
+    int row[kAhead];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = here ? __builtin_fmaf(w, (float)z[i] * f, acc[i]) : acc[i];
-    } else {
-      const float* z = static_cast<const float*>(a.z) + at;
-      if (VEC) {
-        const float4 u = *reinterpret_cast<const float4*>(z), v = *reinterpret_cast<const float4*>(z + 4);
-        const float zz[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = here ? __builtin_fmaf(w, zz[i], acc[i]) : acc[i];
+    for (int j = 0; j < kAhead; ++j) {
+      row[j] = j0 + j < a.topk ? moe::uniform(slot + j0 + j) : -1;
+      if (row[j] < 0) continue;
+      const int64_t at = (int64_t)row[j] * a.n + n0;
+      if constexpr (HALF) {
+        z[j] = *reinterpret_cast<const h8*>(static_cast<const _Float16*>(a.z) + at);
+        scale[j] = a.z_scales[at >> 5];
       } else {
+        const float* p = static_cast<const float*>(a.z) + at;
+        if (VEC) {
+          const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 4);
+          z[j] = f8{u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i < left && here) acc[i] = __builtin_fmaf(w, z[i], acc[i]);
+          for (int i = 0; i < 8; ++i) z[j][i] = p[min(i, left - 1)];
+        }
       }
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (row[j] < 0) continue;
+      const float w = __int_as_float(moe::uniform(weight + j0 + j));
+      // (a scale byte is never 0: see the product's epilogue)
+      const float f = HALF ? __uint_as_float(scale[j] << 23) : 1.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(w, HALF ? (float)z[j][i] * f : (float)z[j][i], acc[i]);
     }
   }
   typedef float f2 __attribute__((ext_vector_type(2)));
