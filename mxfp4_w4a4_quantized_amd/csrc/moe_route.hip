@@ -339,7 +339,7 @@ void launch_route_nv(const RouteArgs& a, hipStream_t s) {
 
 constexpr int kPlanWaves = 16;
 static_assert(64 * kPlanWaves >= moe::kMaxExperts, "a thread for each expert");
-constexpr int kHeld = 8;   // steps of 64 pairs whose ids a wave reads once
+constexpr int kHeld = 4;   // steps of 64 pairs whose ids a wave reads once (8: 0.5 us slower, by its code)
 
 __device__ __forceinline__ int expert_of(const PlanArgs& a, int64_t p, int64_t end) {
   if (p >= end) return -1;
@@ -380,31 +380,34 @@ __global__ __launch_bounds__(64 * kPlanWaves) void moe_place_kernel(PlanArgs a) 
   __shared__ int32_t most;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int E = a.experts;
+  const bool alone = gridDim.x == 1;
   const int64_t chunk0 = blockIdx.x * a.chunk, left = a.pairs - chunk0;
-  const int64_t here = left < a.chunk ? left : a.chunk;                         // pairs of this workgroup
-  const int64_t run = (here + 64 * kPlanWaves - 1) / (64 * kPlanWaves) * 64;    // and of a wave
-  const int64_t begin = chunk0 + wave * run, end = min(chunk0 + here, begin + run);
+  const uint32_t here = (uint32_t)(left < a.chunk ? left : a.chunk);            // pairs of this workgroup
+  const uint32_t run = (here + blockDim.x - 1) / blockDim.x * 64;               // and of a wave
+  const int used = run == 0 ? 0 : (int)((here + run - 1) / run);                // waves that have some
+  const int64_t begin = chunk0 + wave * (int64_t)run, end = min(chunk0 + here, begin + run);
   int held[kHeld];
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) held[i] = expert_of(a, begin + 64 * i + lane, end);
   // a thread adds up one expert's counts over a part of the chunks, this one's
   // and the later ones' apart
-  const int wide = min(E, (int)blockDim.x), parts = (int)blockDim.x / wide;
-  const int part = (int)threadIdx.x / wide, mine = (int)threadIdx.x - part * wide;
-  int sum = 0, sum_before = 0;
-  if (gridDim.x > 1 && part < parts) {
-    const int grid = (int)gridDim.x;
+  int mine = -1, sum = 0, sum_before = 0;
+  if (!alone) {
+    const int wide = min(E, (int)blockDim.x), parts = (int)blockDim.x / wide, grid = (int)gridDim.x;
+    const int part = (int)threadIdx.x / wide;
+    if (part < parts) {
+      mine = (int)threadIdx.x - part * wide;
 #pragma unroll 8
-    for (int g = part; g < grid; g += parts) {
-      const int c = a.counts[(int64_t)g * E + mine];
-      sum += c;
-      sum_before += g < (int)blockIdx.x ? c : 0;
+      for (int g = part; g < grid; g += parts) {
+        const int c = a.counts[(int64_t)g * E + mine];
+        sum += c;
+        sum_before += g < (int)blockIdx.x ? c : 0;
+      }
     }
   }
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
     total[e] = before[e] = 0;
-#pragma unroll
-    for (int w = 0; w < kPlanWaves; ++w) pos[w][e] = 0;
+    for (int w = 0; w < used; ++w) pos[w][e] = 0;
   }
   if (threadIdx.x == 0) most = 0;
   __syncthreads();
@@ -415,20 +418,11 @@ __global__ __launch_bounds__(64 * kPlanWaves) void moe_place_kernel(PlanArgs a) 
     const int e = expert_of(a, p, end);
     if (e >= 0) atomicAdd(&pos[wave][e], 1);
   }
-  if (gridDim.x > 1 && part < parts) {
+  if (mine >= 0) {
     atomicAdd(&total[mine], sum);
     atomicAdd(&before[mine], sum_before);
   }
   __syncthreads();
-  if (gridDim.x == 1) {
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-      int c = 0;
-#pragma unroll
-      for (int w = 0; w < kPlanWaves; ++w) c += pos[w][e];
-      total[e] = c;
-    }
-    __syncthreads();
-  }
   // wave 0: rows; wave 1 + h: tiles of height h
   if (wave <= moe::kHeights) {
     int32_t* out = wave == 0 ? offset : first[wave - 1];
@@ -436,7 +430,13 @@ __global__ __launch_bounds__(64 * kPlanWaves) void moe_place_kernel(PlanArgs a) 
     int carry = 0, top = 0;
     for (int e0 = 0; e0 < E; e0 += 64) {
       const int e = e0 + lane;
-      const int c = e < E ? (total[e] + (1 << shift) - 1) >> shift : 0;
+      int c = 0;
+      if (e < E) {
+        c = total[e];
+        if (alone)
+          for (int w = 0; w < used; ++w) c += pos[w][e];
+        c = (c + (1 << shift) - 1) >> shift;
+      }
       const int v = wave_scan(c);
       if (e < E) out[e] = carry + v - c;
       carry += __builtin_amdgcn_readlane(v, 63);
@@ -448,8 +448,7 @@ __global__ __launch_bounds__(64 * kPlanWaves) void moe_place_kernel(PlanArgs a) 
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
     int next = offset[e] + before[e];
-#pragma unroll
-    for (int w = 0; w < kPlanWaves; ++w) {
+    for (int w = 0; w < used; ++w) {
       const int c = pos[w][e];
       pos[w][e] = next;
       next += c;
@@ -497,7 +496,7 @@ __global__ __launch_bounds__(64 * kPlanWaves) void moe_place_kernel(PlanArgs a) 
     for (int j = 1; j < moe::kHeights; ++j) tiles = h == j ? a.tiles[j] : tiles;
     reinterpret_cast<int4*>(tiles)[i] = make_int4(e, offset[e], offset[e + 1], first[h][e]);
   };
-  if (gridDim.x == 1 && most <= 8) {
+  if (alone && most <= 8) {
     // few tiles each: a thread per expert and height writes them
     for (int i = threadIdx.x; i < moe::kHeights * E; i += blockDim.x) {
       const int h = i / E, e = i - h * E;
@@ -505,7 +504,8 @@ __global__ __launch_bounds__(64 * kPlanWaves) void moe_place_kernel(PlanArgs a) 
     }
   } else {
     // a wave per expert and height
-    for (int i = blockIdx.x * kPlanWaves + wave; i < moe::kHeights * E; i += gridDim.x * kPlanWaves) {
+    const int waves = (int)blockDim.x >> 6;
+    for (int i = blockIdx.x * waves + wave; i < moe::kHeights * E; i += gridDim.x * waves) {
       const int h = i / E, e = i - h * E;
       for (int k = first[h][e] + lane; k < first[h][e + 1]; k += 64) entry(h, k, e);
     }
@@ -642,7 +642,8 @@ hipError_t launch_moe_route(const RouteArgs& a, hipStream_t s) {
 hipError_t launch_moe_plan(const PlanArgs& a, hipStream_t s) {
   const int grid = (int)moe::chunks(a.pairs);
   if (grid > 1) moe_count_kernel<<<grid, 64 * kPlanWaves, 0, s>>>(a);
-  moe_place_kernel<<<grid, 64 * kPlanWaves, 0, s>>>(a);
+  // (8 waves for few pairs: at least one each for the rows and the heights)
+  moe_place_kernel<<<grid, a.pairs <= 512 ? 512 : 64 * kPlanWaves, 0, s>>>(a);
   return hipGetLastError();
 }
 
