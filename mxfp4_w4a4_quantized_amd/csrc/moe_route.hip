@@ -21,11 +21,11 @@ namespace {
 // so that one maximum finds the expert and settles ties.
 //
 // G lanes serve a token, expert G i + lane of them in register i.  64 lanes give
-// the shortest time for few tokens; for many, 16 lanes: of the instructions of a
-// choice those between lanes are then shared by four tokens.  Bound by launch and
-// load latency for few tokens (16 x 128, topk 8: 4.0 us; 2.9 of them with topk 1),
-// by 64-bit arithmetic for many (8192 x 256, topk 8: softmax 9.2 us; sigmoid, bias
-// and 8 groups 16.6, of them 4 the scores, 3 the groups, 3 the choice).
+// the shortest time for few tokens; for many, 16 or 32: of the instructions of a
+// choice those between lanes are then shared by four or two tokens.  Bound by launch
+// and load latency for few tokens (16 x 128, topk 8: 4.0 us; 2.9 of them with topk
+// 1), by 64-bit arithmetic for many (8192 x 256, topk 8: softmax 9.1 us; sigmoid,
+// bias and 8 groups 15.8, of them 6 the scores, 3 the groups, 4 the choice).
 
 // Below every key: none is left.  Keys are kept within +-1e308.
 constexpr uint32_t kNoneHigh = 0xFFEFFFFFu;   // of -1.79e308
@@ -108,10 +108,13 @@ __device__ __forceinline__ T across(T v, Op op) {
   v = op(v, rotated<0x124>(v));
   v = op(v, rotated<0x122>(v));
   v = op(v, rotated<0x121>(v));
-  if constexpr (G == 64) {
-    T a, b;
+  T a, b;
+  if constexpr (G >= 32) {
     paired<1>(v, a, b);
-    paired<2>(op(a, b), a, b);
+    v = op(a, b);
+  }
+  if constexpr (G == 64) {
+    paired<2>(v, a, b);
     v = op(a, b);
   }
   return v;
@@ -268,7 +271,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void moe_route_kernel(RouteArgs a
         rank += other > score || (other == score && h < g) ? 1 : 0;
       }
       const uint64_t in = __builtin_amdgcn_ballot_w64(g < a.groups && rank < a.topk_groups);
-      kept |= G == 64 ? in : ((in >> (threadIdx.x & 48)) & 0xFFFFu) << g0;
+      constexpr uint64_t kToken = ~uint64_t(0) >> (64 - G);   // the token's lanes
+      kept |= ((in >> (threadIdx.x & 63 & ~(G - 1))) & kToken) << g0;
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -625,10 +629,13 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(CombineArgs a) {
 
 hipError_t launch_moe_route(const RouteArgs& a, hipStream_t s) {
   const int e = a.experts;
-  if (a.tokens >= 6144 && e <= 256 && a.topk <= 16) {
+  // (4096 tokens, sigmoid, bias, 8 groups: 64 experts 6.6 us on 16 lanes, 7.8 on 64;
+  // 2048 tokens 6.5 and 6.1; 6000 tokens,
+  // 256 experts 13.3 on 32, 14.8 on 64)
+  if (a.tokens >= 3000 && e <= 256 && a.topk <= 16) {
     if (e <= 64) launch_route_nv<16, 4>(a, s);
     else if (e <= 128) launch_route_nv<16, 8>(a, s);
-    else launch_route_nv<16, 16>(a, s);
+    else launch_route_nv<32, 8>(a, s);
   } else {
     if (e <= 64) launch_route_nv<64, 1>(a, s);
     else if (e <= 128) launch_route_nv<64, 2>(a, s);

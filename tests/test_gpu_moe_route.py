@@ -87,7 +87,11 @@ CASES = [
     (9, 512, 64, "sigmoid", False, 64, 32, "max", True, 1.0),
     (6, 1024, 33, "softmax", True, 1, 1, "max", True, 1.0),
     (3, 64, 3, "sigmoid", True, 64, 5, "top2", True, 1.0),      # groups of one
-    (2050, 48, 4, "softmax", False, 1, 1, "max", True, 1.0),
+    (3050, 48, 4, "softmax", False, 1, 1, "max", True, 1.0),       # 16 and 32 lanes a token
+    (3001, 64, 6, "sigmoid", True, 16, 5, "top2", True, 1.0),
+    (3003, 100, 16, "softmax", True, 4, 3, "max", False, 1.0),
+    (3002, 256, 8, "sigmoid", True, 8, 4, "top2", True, 2.5),
+    (3005, 200, 16, "softmax", False, 40, 11, "max", False, 1.0),
 ]
 
 
