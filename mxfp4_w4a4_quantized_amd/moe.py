@@ -17,6 +17,7 @@ rows = n (ROWMAJOR) or padded_rows(n) (TILED); quantize_experts makes them.
 Inference only: results carry no gradient.
 """
 import ctypes
+import functools
 from dataclasses import dataclass
 from typing import Optional
 
@@ -143,18 +144,26 @@ def moe_route(logits, r: Router, ids=None, weights=None):
     desc = _router_desc(r, experts, dev)
     if r.topk < 1:
         raise ValueError(f"topk must be at least 1, got {r.topk}")
+    # (empty_strided and empty_like: 0.5 us less each than empty, of a call of 8)
     shape = (tokens, r.topk)
     if ids is None:
-        ids = torch.empty(shape, dtype=torch.int32, device=logits.device)
+        ids = torch.empty_strided(shape, (r.topk, 1), dtype=torch.int32, device=logits.device)
+        ip = ids.data_ptr()
+    else:
+        ip = _pairs("ids", ids, shape, torch.int32, dev)
     if weights is None:
-        weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
-    ip, wp = _pairs("ids", ids, shape, torch.int32, dev), _pairs("weights", weights, shape, torch.float32, dev)
+        weights = torch.empty_like(ids, dtype=torch.float32)
+        wp = weights.data_ptr()
+    else:
+        wp = _pairs("weights", weights, shape, torch.float32, dev)
     _check(lib().mxfp4_moe_route(ptr, _code(logits.dtype), tokens, experts, ld, desc, ip, wp, _stream(dev)),
            "mxfp4_moe_route")
     return ids, weights
 
 
+@functools.lru_cache(maxsize=4096)
 def _plan_words(tokens, topk, experts):
+    """int32 words of a plan (a number of the sizes alone)."""
     n = ctypes.c_int64()
     _check(lib().mxfp4_moe_plan_bytes(tokens, topk, experts, ctypes.byref(n)), "mxfp4_moe_plan_bytes")
     return n.value // 4
@@ -170,8 +179,8 @@ def moe_plan(ids, experts: int, first: int = 0, plan: ExpertPlan = None):
     tokens, topk = ids.shape
     ip = _pairs("ids", ids, (tokens, topk), torch.int32, dev)
     if plan is None:
-        plan = ExpertPlan(torch.empty(_plan_words(tokens, topk, experts), dtype=torch.int32, device=ids.device), tokens,
-                          topk, experts)
+        words = torch.empty_strided((_plan_words(tokens, topk, experts),), (1,), dtype=torch.int32, device=ids.device)
+        plan = ExpertPlan(words, tokens, topk, experts)
     elif (plan.tokens, plan.topk, plan.experts) != (tokens, topk, experts) or plan.words.get_device() != dev:
         raise ValueError(f"the plan is for {plan.tokens} tokens, {plan.topk} choices and {plan.experts} experts on "
                          f"{plan.words.device}")
