@@ -198,10 +198,19 @@ def quantize_experts(w, rot=None, layout: int = ROWMAJOR, fit: bool = False):
     return torch.stack([c for c, _ in each]), torch.stack([s for _, s in each])
 
 
+# What depends on the sizes of a call alone is worked out once for each of them: a
+# small block's kernels take no longer than its Python.
+
+
+@functools.lru_cache(maxsize=4096)
+def _stack_shapes(experts, n, k, layout):
+    cshape, sshape = _out_shapes(n, k, layout)
+    return (experts, *cshape), (experts, *sshape)
+
+
 def _stack(name, codes, scales, experts, n, k, layout, dev):
     """Checks stacked weights: (pointers)"""
-    cshape, sshape = _out_shapes(n, k, layout)
-    cshape, sshape = (experts, *cshape), (experts, *sshape)
+    cshape, sshape = _stack_shapes(experts, n, k, layout)
     if (codes.shape != cshape or scales.shape != sshape or codes.get_device() != dev or scales.get_device() != dev or
             codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not codes.is_contiguous() or
             not scales.is_contiguous()):
@@ -280,7 +289,9 @@ def moe_up_requant(a_codes, a_scales, plan: ExpertPlan, w_up, w_gate=None, act="
     return y_codes, y_scales
 
 
-def _down_workspace(tokens, topk, experts, n, k, layout, yt):
+@functools.lru_cache(maxsize=4096)
+def _down_workspace(tokens, topk, experts, n, k, layout, yt, dev):
+    """Bytes of the workspace on GPU dev (the current one)."""
     b = ctypes.c_int64()
     _check(lib().mxfp4_moe_down_workspace(tokens, topk, experts, n, k, layout, yt, ctypes.byref(b)),
            "mxfp4_moe_down_workspace")
@@ -311,20 +322,41 @@ def moe_down(h_codes, h_scales, plan: ExpertPlan, weights, w_down, bias=None, re
     desc = MoeDownDesc(dc, ds, bp, 0 if bt is None else _code(bt), 0)
     res, rt, ld_r = _residual(residual, (plan.tokens, n), dev)
     y, ptr, ld, yt = _dense_output(y, plan.tokens, n, out_dtype, h_codes)
-    need = _down_workspace(plan.tokens, plan.topk, plan.experts, n, k, layout, yt)
+    need = _down_workspace(plan.tokens, plan.topk, plan.experts, n, k, layout, yt, dev)
+    wsp, size = None, 0
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=h_codes.device)
+        if need > 0:
+            workspace = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=h_codes.device)
+            wsp, size = workspace.data_ptr(), need
     elif workspace.get_device() != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the operands' GPU")
+    else:
+        wsp, size = workspace.data_ptr(), workspace.numel()
     _check(lib().mxfp4_moe_down(hc, hs, _plan_ptr(plan, dev), plan.tokens, plan.topk, plan.experts, wp, desc, n, k, layout,
-                                res, rt, ld_r, ptr, yt, ld, workspace.data_ptr(), workspace.numel(), _stream(dev)),
+                                res, rt, ld_r, ptr, yt, ld, wsp, size, _stream(dev)),
            "mxfp4_moe_down")
     return y
 
 
 def moe_down_workspace(plan: ExpertPlan, n: int, k: int, out_dtype=torch.bfloat16, layout: int = ROWMAJOR):
     """Bytes of moe_down's workspace for hidden activations of width k."""
-    return _down_workspace(plan.tokens, plan.topk, plan.experts, n, k, layout, _code(out_dtype))
+    return _down_workspace(plan.tokens, plan.topk, plan.experts, n, k, layout, _code(out_dtype), _gpu(plan.words))
+
+
+@functools.lru_cache(maxsize=4096)
+def _ffn_work(tokens, topk, experts, d, hidden, layout, yt, dev):
+    """Offsets of what lies between moe_ffn's calls in its allocation (ids, weights,
+    plan, codes and scales of x and of the hidden activations, workspace), the
+    allocation's size, and the plan's and the workspace's."""
+    rows = tokens * topk
+    tp, rp = (padded_rows(tokens), padded_rows(rows)) if layout == TILED else (tokens, rows)
+    plan = 4 * _plan_words(tokens, topk, experts)
+    work = _down_workspace(tokens, topk, experts, d, hidden, layout, yt, dev)
+    starts, total = [], 0
+    for size in (rows * 4, rows * 4, plan, tp * d // 2, tp * d // 32, rp * hidden // 2, rp * hidden // 32, work):
+        starts.append(total)
+        total += (size + 255) // 256 * 256
+    return tuple(starts), total, plan, work
 
 
 def moe_ffn(x, logits, r: Router, w_up, w_down, hidden: int, w_gate=None, act="silu", rot=None, bias_up=None,
@@ -349,7 +381,6 @@ def moe_ffn(x, logits, r: Router, w_up, w_down, hidden: int, w_gate=None, act="s
         raise ValueError(f"topk must be at least 1, got {r.topk}")
     dev = _gpu(x)
     (tokens, d), topk, experts = x.shape, r.topk, w_up[0].shape[0]
-    rows = tokens * topk
     # the calls of quantize_rotate, moe_route, moe_plan, moe_up_requant and
     # moe_down, with everything between them in one allocation and not checked again
     xp, ld_x = _matrix("x", x, x.shape, dev)
@@ -366,24 +397,18 @@ def moe_ffn(x, logits, r: Router, w_up, w_down, hidden: int, w_gate=None, act="s
     y, yp, ld_y, yt = _dense_output(y, tokens, d, out_dtype, x)
     if tokens == 0:
         return y
-    tp, rp = (padded_rows(tokens), padded_rows(rows)) if layout == TILED else (tokens, rows)
-    sizes = [rows * 4, rows * 4, 4 * _plan_words(tokens, topk, experts), tp * d // 2, tp * d // 32, rp * hidden // 2,
-             rp * hidden // 32, _down_workspace(tokens, topk, experts, d, hidden, layout, yt)]
-    starts, total = [], 0
-    for size in sizes:
-        starts.append(total)
-        total += (size + 255) // 256 * 256
-    work = torch.empty(total, dtype=torch.uint8, device=x.device)
+    starts, total, plan_size, work_size = _ffn_work(tokens, topk, experts, d, hidden, layout, yt, dev)
+    work = torch.empty_strided((total,), (1,), dtype=torch.uint8, device=x.device)
     base = work.data_ptr()
-    ids, weights, plan, ac, as_, hc, hs, ws = (base + at for at in starts)
+    ids, weights, plan, ac, as_, hc, hs, ws = [base + at for at in starts]
     L, stream = lib(), _stream(dev)
     _check(L.mxfp4_moe_route(lp, _code(logits.dtype), tokens, logits.shape[1], ld_l, router, ids, weights, stream),
            "mxfp4_moe_route")
-    _check(L.mxfp4_moe_plan(ids, tokens, topk, first, experts, plan, sizes[2], stream), "mxfp4_moe_plan")
+    _check(L.mxfp4_moe_plan(ids, tokens, topk, first, experts, plan, plan_size, stream), "mxfp4_moe_plan")
     _check(L.mxfp4_quantize_rotate(xp, _code(x.dtype), tokens, d, ld_x, rdesc, layout, ac, as_, stream),
            "mxfp4_quantize_rotate")
     _check(L.mxfp4_moe_up_requant(ac, as_, plan, tokens, topk, experts, up, hidden, d, layout, rdesc, hc, hs, layout,
                                   stream), "mxfp4_moe_up_requant")
     _check(L.mxfp4_moe_down(hc, hs, plan, tokens, topk, experts, weights, down, d, hidden, layout, res, rt, ld_r, yp, yt,
-                            ld_y, ws, sizes[7], stream), "mxfp4_moe_down")
+                            ld_y, ws, work_size, stream), "mxfp4_moe_down")
     return y
