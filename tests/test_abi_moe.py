@@ -126,12 +126,12 @@ def test_up_refusals():
     assert upq(w, tokens=0) == OK
 
 
-def down_bytes(tokens=4, topk=2, experts=8, n=64, k=128, layout=R, y_dtype=BF):
+def down_bytes(tokens=40, topk=4, experts=64, n=64, k=128, layout=R, y_dtype=BF):
     b = ctypes.c_int64(-1)
     return mx.lib().mxfp4_moe_down_workspace(tokens, topk, experts, n, k, layout, y_dtype, ctypes.byref(b)), b.value
 
 
-def down(w, hc=A, hs=A, p=A, tokens=4, topk=2, experts=8, weights=A, n=64, k=128, layout=R, res=None, rt=BF, ld_r=64, y=A,
+def down(w, hc=A, hs=A, p=A, tokens=40, topk=4, experts=64, weights=A, n=64, k=128, layout=R, res=None, rt=BF, ld_r=64, y=A,
          y_dtype=BF, ld_y=64, ws=A, size=1 << 40):
     return mx.lib().mxfp4_moe_down(hc, hs, p, tokens, topk, experts, weights, ref(w), n, k, layout, res, rt, ld_r, y, y_dtype,
                                    ld_y, ws, size, None)
@@ -165,7 +165,8 @@ def test_down_workspace():
         assert down_bytes(**bad)[0] == UNS, bad
     assert down_bytes(tokens=0) == (OK, 0) and down_bytes(n=0) == (OK, 0)
     # fp32 products for few rows or an fp32 result, else 16 bits and a byte for 32 columns
-    assert down_bytes()[1] >= 8 * 64 * 4
+    assert down_bytes()[1] >= 160 * 64 * 4
+    assert down_bytes(tokens=4) == (OK, 0)             # few pairs: products and sum in one launch
     big = dict(tokens=4096, topk=2, experts=8, n=256)
     assert down_bytes(**big, y_dtype=F)[1] >= 8192 * 256 * 4
     assert 8192 * (512 + 8) <= down_bytes(**big)[1] < 8192 * 256 * 4

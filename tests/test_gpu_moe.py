@@ -276,6 +276,7 @@ DOWN = [(1, 1, 1, 128, 128), (1, 2, 8, 1024, 96), (5, 3, 3, 96, 40), (40, 3, 10,
         (61, 4, 12, 384, 300), (100, 3, 8, 1152, 33), (300, 2, 5, 256, 300), (300, 2, 5, 128, 288), (700, 3, 4, 640, 520),
         (700, 3, 4, 640, 544), (1100, 2, 3, 1280, 515), (2600, 2, 3, 128, 320),
         (150, 2, 4, 64, 200), (400, 2, 3, 1184, 224), (1500, 2, 4, 416, 160),
+        (60, 4, 48, 256, 200), (60, 4, 48, 96, 33),
         # few pairs and a wide result: products and sum in one launch, with K in parts and whole
         (1, 1, 1, 128, 4096), (1, 2, 8, 2048, 4096), (5, 3, 4, 160, 4100), (16, 8, 128, 384, 3200), (128, 1, 16, 128, 7300)]
 
