@@ -37,6 +37,10 @@
 //  * 3584 x 12288 -> 3072, bias, gate, residual 79-84 us, 3.2-3.4 PF/s (69.5)
 //  * 3584 x 3072 -> 12288, tanh GELU, H32, MXFP4  91-100 us, 2.7-3.0 PF/s (72.6)
 //  * 523 x 1408 -> 2 x 3001 fp32, gated, bias      12-13 us (128 x 128 tiles)
+//  * experts' products (MoeArgs): 8192 tokens x 8 of 64 experts, 4096 -> 2 x 2048,
+//    gated silu, 620-650 us, 3.4-3.55 PF/s (65536 rows of one expert 542, of 64
+//    experts with 1024 rows each in token order 585); 301 x 3 of 10, 1184 -> 2 x 1000
+//    fp32, bias, 12.3 us (a tail of K)
 // (over the cards; within a card to 1%.)
 #pragma once
 #include "gemm_large_core.h"

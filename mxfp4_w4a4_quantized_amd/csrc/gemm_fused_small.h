@@ -16,6 +16,8 @@
 // Measured (tiled weights from HBM): 16 x 4096 -> 2 x 14336, gated silu, 62.9 MB
 // in 14.2 us, 4.4 TB/s; 1 x 14336 -> 4096 with a residual, 31.2 MB in 9.6 us,
 // 3.2 TB/s (start, join of the K split and end: 3 to 4 us over the bytes alone).
+// Experts' products (MoeArgs): 64 tokens x 8 of 128 experts, 4096 -> 2 x 2048, gated
+// silu, MXFP4, 1.05 GB of weights in 148 us, 7.1 TB/s.
 #pragma once
 #include "gemm_small_core.h"
 #include "activation.h"
