@@ -376,6 +376,15 @@ __device__ __forceinline__ int wave_scan(int v) {
   return v;
 }
 
+// What a wave's lanes wrote to LDS before it, its lanes read after it.  (The hardware
+// does a wave's LDS operations in order; the fences keep the compiler from moving
+// them: a wave barrier alone says nothing about memory.)
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 __global__ __launch_bounds__(64 * kPlanWaves) void moe_place_kernel(PlanArgs a) {
   __shared__ int32_t pos[kPlanWaves][moe::kMaxExperts];     // counts, then next rows, of each wave's run
   __shared__ int32_t total[moe::kMaxExperts], before[moe::kMaxExperts];
@@ -470,15 +479,15 @@ __global__ __launch_bounds__(64 * kPlanWaves) void moe_place_kernel(PlanArgs a) 
       same &= set ? m : ~m;
     }
     int row = -1;
+    const int rank = __popcll(same & below);
+    if (e >= 0) row = pos[wave][e] + rank;
+    wave_lds_sync();   // every lane has read its expert's next row ..
     if (e >= 0) {
-      const int rank = __popcll(same & below);
-      row = pos[wave][e] + rank;
-      __builtin_amdgcn_wave_barrier();
       if (rank == 0) pos[wave][e] = row + __popcll(same);
       a.order[row] = (int32_t)p;
       a.token[row] = (int32_t)((uint32_t)p / (uint32_t)a.topk);
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_sync();   // .. and the next 64 pairs read what the first of them wrote
     if (p < end) a.slot[p] = row;
   };
 #pragma unroll
