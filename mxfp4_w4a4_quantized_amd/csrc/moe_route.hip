@@ -318,16 +318,23 @@ __global__ __launch_bounds__(64 * kRouteWaves) void moe_route_kernel(RouteArgs a
 }
 
 template <int G, int NV>
-void launch_route_nv(const RouteArgs& a, hipStream_t s) {
+void launch_route_nv(RouteArgs a, hipStream_t s) {
   constexpr int PER = 64 * kRouteWaves / G;
-  const int grid = (int)((a.tokens + PER - 1) / PER);
+  constexpr int64_t kMost = (int64_t(1) << 23) * PER;   // tokens of a launch: a grid holds less than 2^32 threads
   const size_t bytes = sizeof(double) * PER * (a.experts + a.groups + 1 + 64);
-  if (a.groups > 1) {
-    if (a.bias != nullptr) moe_route_kernel<G, NV, true, true><<<grid, 64 * kRouteWaves, bytes, s>>>(a);
-    else moe_route_kernel<G, NV, false, true><<<grid, 64 * kRouteWaves, bytes, s>>>(a);
-  } else {
-    if (a.bias != nullptr) moe_route_kernel<G, NV, true, false><<<grid, 64 * kRouteWaves, 0, s>>>(a);
-    else moe_route_kernel<G, NV, false, false><<<grid, 64 * kRouteWaves, 0, s>>>(a);
+  for (int64_t left = a.tokens; left > 0; left -= kMost) {
+    a.tokens = left < kMost ? left : kMost;
+    const int grid = (int)((a.tokens + PER - 1) / PER);
+    if (a.groups > 1) {
+      if (a.bias != nullptr) moe_route_kernel<G, NV, true, true><<<grid, 64 * kRouteWaves, bytes, s>>>(a);
+      else moe_route_kernel<G, NV, false, true><<<grid, 64 * kRouteWaves, bytes, s>>>(a);
+    } else {
+      if (a.bias != nullptr) moe_route_kernel<G, NV, true, false><<<grid, 64 * kRouteWaves, 0, s>>>(a);
+      else moe_route_kernel<G, NV, false, false><<<grid, 64 * kRouteWaves, 0, s>>>(a);
+    }
+    a.logits = static_cast<const uint8_t*>(a.logits) + a.tokens * a.ld * (a.bf16 ? 2 : 4);
+    a.ids += a.tokens * a.topk;
+    a.weights += a.tokens * a.topk;
   }
 }
 
