@@ -117,9 +117,11 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_small_kernel(MoeArgs
 // little for each workgroup to read: 4 x 4 of 32, 1024 -> 1024 5.5 us against 5.9 in
 // two launches, 12 x 3 of 10, 2816 -> 2816 11.3 and 13.2, but 16 x 8 of 32, 2048 ->
 // 1024 17.8 and 10.3.
+// (Below 2^26 columns: a grid holds less than 2^32 threads.)
 bool moe_down_small(const MoeArgs& f) {
   const int64_t tiles = f.g.m < f.experts ? f.g.m : f.experts;   // at most
-  return f.g.m <= kDownPairs && moe_tile_rows(f) == 16 && (f.g.n >= 12 * cu_count() || tiles * f.g.k <= 32768);
+  return f.g.m <= kDownPairs && f.g.n < (1 << 26) && moe_tile_rows(f) == 16 &&
+         (f.g.n >= 12 * cu_count() || tiles * f.g.k <= 32768);
 }
 
 hipError_t launch_moe_down_small(const MoeArgs& f, const CombineArgs& c, hipStream_t s) {
