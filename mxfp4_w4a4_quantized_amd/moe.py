@@ -368,9 +368,9 @@ def moe_ffn(x, logits, r: Router, w_up, w_down, hidden: int, w_gate=None, act="s
          y = residual + sum over a token's choices of weight * (h D_e^T + bd)
     x: [tokens, d] dense (the block's norm is done: the router's logits need it
     too); logits: [tokens, all experts]; w_up, w_gate ([hidden, d] each) and w_down
-    ([d, hidden]): stacks over this GPU's experts, first .. first + experts - 1 (the
-    other experts add nothing here), quantized with the weight side of `rot` (None
-    or "h32").  y: residual's type, or x's."""
+    ([d, hidden]): stacks over this GPU's experts, first .. first + experts - 1 of
+    the logits' (the others add nothing here), quantized with the weight side of
+    `rot` (None or "h32").  y: residual's type, or x's."""
     if x.dim() != 2:
         raise ValueError("x must be 2-D with unit column stride")
     if rot is not None and rot != HADAMARD32:
@@ -379,8 +379,11 @@ def moe_ffn(x, logits, r: Router, w_up, w_down, hidden: int, w_gate=None, act="s
         raise ValueError("logits must be [tokens, experts], with x's tokens")
     if r.topk < 1:
         raise ValueError(f"topk must be at least 1, got {r.topk}")
+    experts = w_up[0].shape[0]
+    if first < 0 or first + experts > logits.shape[1]:
+        raise ValueError(f"experts {first} .. {first + experts - 1} of weights are not among the logits' {logits.shape[1]}")
     dev = _gpu(x)
-    (tokens, d), topk, experts = x.shape, r.topk, w_up[0].shape[0]
+    (tokens, d), topk = x.shape, r.topk
     # the calls of quantize_rotate, moe_route, moe_plan, moe_up_requant and
     # moe_down, with everything between them in one allocation and not checked again
     xp, ld_x = _matrix("x", x, x.shape, dev)

@@ -1,0 +1,21 @@
+"""What the mixture-of-experts binding refuses by sizes alone, on the CPU."""
+import pytest
+import torch
+
+import mxfp4_w4a4_quantized_amd as mx
+
+
+def stack(experts, n, k):
+    return torch.zeros(experts, n, k // 2, dtype=torch.uint8), torch.zeros(experts, n, k // 32, dtype=torch.uint8)
+
+
+@pytest.mark.parametrize("first,experts", [(-1, 4), (5, 4), (8, 1), (0, 9), (1 << 29, 4)])
+def test_ffn_refuses_experts_that_the_logits_do_not_have(first, experts):
+    """8 experts routed: this GPU's have to be among them (else they add nothing, silently)."""
+    x, logits = torch.zeros(3, 64), torch.zeros(3, 8)
+    with pytest.raises(ValueError, match="not among the logits' 8"):
+        mx.moe_ffn(x, logits, mx.Router(2), stack(experts, 32, 64), stack(experts, 64, 32), 32, first=first)
+    with pytest.raises(ValueError, match="GPU"):                    # (the whole and a part pass this check)
+        mx.moe_ffn(x, logits, mx.Router(2), stack(8, 32, 64), stack(8, 64, 32), 32)
+    with pytest.raises(ValueError, match="GPU"):
+        mx.moe_ffn(x, logits, mx.Router(2), stack(4, 32, 64), stack(4, 64, 32), 32, first=4)
