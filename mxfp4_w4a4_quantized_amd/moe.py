@@ -82,12 +82,13 @@ class Router:
     scale: float = 1.0
 
 
-@dataclass
+@dataclass(frozen=True)
 class ExpertPlan:
     """The pairs (token * topk + choice) in expert order.  offsets [experts + 1]:
     first row of each expert, then the number of rows; order [tokens * topk]: pair
     of each row, -1 behind the last; slot [tokens * topk]: row of each pair, -1
-    where its expert is not among these.  All int32, views of `words`."""
+    where its expert is not among these.  All int32, views of `words`.  Plans come
+    from moe_plan; their sizes do not change."""
     words: torch.Tensor
     tokens: int
     topk: int
@@ -169,6 +170,19 @@ def _plan_words(tokens, topk, experts):
     return n.value // 4
 
 
+def _plan_ptr(plan, dev):
+    """Checks that a plan's words are as many as its sizes ask for: the products
+    read tile tables, tokens and slots from them."""
+    words = plan.words
+    if words.get_device() != dev:
+        raise _bad("the plan", words, words.shape, dev)
+    need = _plan_words(plan.tokens, plan.topk, plan.experts)
+    if words.dtype != torch.int32 or words.shape != (need,) or not words.is_contiguous():
+        raise ValueError(f"a plan of {plan.tokens} tokens, {plan.topk} choices and {plan.experts} experts has {need} "
+                         f"contiguous int32 words, got {words.dtype} {tuple(words.shape)}")
+    return words.data_ptr()
+
+
 def moe_plan(ids, experts: int, first: int = 0, plan: ExpertPlan = None):
     """The plan for ids [tokens, topk] (int32) over the experts first .. first +
     experts - 1; other ids, -1 among them, have no row.  `plan`: one of the same
@@ -184,7 +198,7 @@ def moe_plan(ids, experts: int, first: int = 0, plan: ExpertPlan = None):
     elif (plan.tokens, plan.topk, plan.experts) != (tokens, topk, experts) or plan.words.get_device() != dev:
         raise ValueError(f"the plan is for {plan.tokens} tokens, {plan.topk} choices and {plan.experts} experts on "
                          f"{plan.words.device}")
-    _check(lib().mxfp4_moe_plan(ip, tokens, topk, first, experts, plan.words.data_ptr(), plan.words.numel() * 4,
+    _check(lib().mxfp4_moe_plan(ip, tokens, topk, first, experts, _plan_ptr(plan, dev), plan.words.numel() * 4,
                                 _stream(dev)), "mxfp4_moe_plan")
     return plan
 
@@ -233,12 +247,6 @@ def _expert_bias(name, t, experts, n, dtype, dev):
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} is {t.dtype}, expected {dtype} (the vectors of a call share a dtype)")
     return t.data_ptr(), t.dtype
-
-
-def _plan_ptr(plan, dev):
-    if plan.words.get_device() != dev:
-        raise _bad("the plan", plan.words, plan.words.shape, dev)
-    return plan.words.data_ptr()
 
 
 def _up_desc(act, w_up, w_gate, bias_up, bias_gate, experts, n, k, layout, dev):

@@ -1,8 +1,11 @@
 """What the mixture-of-experts binding refuses by sizes alone, on the CPU."""
+import dataclasses
+
 import pytest
 import torch
 
 import mxfp4_w4a4_quantized_amd as mx
+from mxfp4_w4a4_quantized_amd import moe
 
 
 def stack(experts, n, k):
@@ -19,3 +22,22 @@ def test_ffn_refuses_experts_that_the_logits_do_not_have(first, experts):
         mx.moe_ffn(x, logits, mx.Router(2), stack(8, 32, 64), stack(8, 64, 32), 32)
     with pytest.raises(ValueError, match="GPU"):
         mx.moe_ffn(x, logits, mx.Router(2), stack(4, 32, 64), stack(4, 64, 32), 32, first=4)
+
+
+def test_products_refuse_a_plan_whose_words_are_not_of_its_sizes():
+    """(the check itself, with the host's number for a device: -1)"""
+    need = moe._plan_words(10, 3, 5)
+    words = torch.zeros(need, dtype=torch.int32)
+    assert moe._plan_ptr(mx.ExpertPlan(words, 10, 3, 5), -1) == words.data_ptr()
+    for sizes in ((11, 3, 5), (10, 4, 5), (10, 3, 6), (9, 3, 5), (1000, 8, 64)):
+        with pytest.raises(ValueError, match="int32 words"):
+            moe._plan_ptr(mx.ExpertPlan(words, *sizes), -1)
+    for bad in (words[1:], words.float(), words.long(), torch.zeros(2 * need, dtype=torch.int32)[::2], words.reshape(1, -1)):
+        with pytest.raises(ValueError, match="int32 words"):
+            moe._plan_ptr(mx.ExpertPlan(bad, 10, 3, 5), -1)
+    with pytest.raises(RuntimeError):
+        moe._plan_ptr(mx.ExpertPlan(words, 10, 65, 5), -1)
+    with pytest.raises(ValueError, match="host"):
+        moe._plan_ptr(mx.ExpertPlan(words, 10, 3, 5), 0)
+    with pytest.raises(dataclasses.FrozenInstanceError):
+        mx.ExpertPlan(words, 10, 3, 5).topk = 30
