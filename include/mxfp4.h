@@ -586,8 +586,17 @@ typedef struct {
     const uint8_t* g_scales;
     const void* bias_u;       /* device [experts][n], or NULL */
     const void* bias_g;       /* device [experts][n], or NULL */
-    int32_t reserved;         /* must be 0 */
+    union {
+        int32_t router_experts;   /* experts that the tokens are spread over, or 0: the plan's */
+        int32_t reserved;         /* (the field's name while it had to be 0) */
+    };
 } mxfp4_moe_up_weights;
+
+/* router_experts, here and below: a GPU that holds a part of the experts passes
+ * the number that the router chooses from, at least the plan's and at most 1024
+ * (INVALID_ARG, UNSUPPORTED).  The kernel is chosen by the rows that an expert can
+ * expect, tokens * topk / router_experts; a part's rows then are the same sums as
+ * the whole's.  Results are right with any number. */
 
 /*   a_codes/a_scales  the tokens' activations, [tokens] rows of k in `layout`
  *   plan              of (tokens, topk, experts)
@@ -619,7 +628,10 @@ typedef struct {
     const uint8_t* scales;
     const void* bias;         /* device [experts][n] of vec_dtype, or NULL */
     int32_t vec_dtype;
-    int32_t reserved;         /* must be 0 */
+    union {
+        int32_t router_experts;   /* as above */
+        int32_t reserved;
+    };
 } mxfp4_moe_down_weights;
 
 /*   h_codes/h_scales  [tokens * topk] rows of k in `layout`, in the plan's order
@@ -632,7 +644,9 @@ typedef struct {
  *                     significant: an eighth of bf16's rounding
  *   workspace         device, 256-byte aligned, of mxfp4_moe_down_workspace bytes
  *                     (the products; 0 for few pairs: then it may be NULL); needs
- *                     no clearing, and calls that may overlap in time need one each
+ *                     no clearing, and calls that may overlap in time need one each.
+ *                     With router_experts, mxfp4_moe_down_workspace is asked with
+ *                     that number as its experts
  * Errors: as mxfp4_moe_up (null weights are INVALID_ARG, and so is a workspace
  *   that is missing or too short). */
 MXFP4_API mxfp4_status mxfp4_moe_down_workspace(int64_t tokens, int64_t topk, int64_t experts, int64_t n, int64_t k,

@@ -23,13 +23,20 @@ mxfp4_status check_plan_sizes(int64_t tokens, int64_t topk, int64_t experts) {
   return MXFP4_OK;
 }
 
+// The experts that the tokens are spread over: the plan's where none are given.
+mxfp4_status check_spread(int32_t router_experts, int64_t experts) {
+  if (router_experts != 0 && router_experts < experts) return MXFP4_ERR_INVALID_ARG;
+  return router_experts > mxfp4::moe::kMaxExperts ? MXFP4_ERR_UNSUPPORTED : MXFP4_OK;
+}
+
 // The plan's part of a product's arguments.
-void set_plan(const void* plan, int64_t pairs, int64_t experts, mxfp4::MoeArgs& f) {
+void set_plan(const void* plan, int64_t pairs, int64_t experts, int32_t router_experts, mxfp4::MoeArgs& f) {
   const mxfp4::moe::PlanLayout l = mxfp4::moe::plan_layout(pairs, experts);
   const int32_t* p = static_cast<const int32_t*>(plan);
   for (int i = 0; i < mxfp4::moe::kHeights; ++i) f.tiles[i] = p + l.tiles[i];
   f.ntiles = p + l.ntiles;
   f.experts = static_cast<int32_t>(experts);
+  f.spread = router_experts != 0 ? router_experts : f.experts;
 }
 
 // Operands of a product: `rows` rows of A, `pairs` of the result, experts' weights
@@ -80,7 +87,7 @@ mxfp4_status launch(const mxfp4::MoeArgs& f, int height, void* stream) {
 }
 
 mxfp4_status check_up(const mxfp4_moe_up_weights* w) {
-  if (w == nullptr || !is_act(w->act) || !is_dtype(w->vec_dtype) || w->reserved != 0) return MXFP4_ERR_INVALID_ARG;
+  if (w == nullptr || !is_act(w->act) || !is_dtype(w->vec_dtype)) return MXFP4_ERR_INVALID_ARG;
   if (w->g_codes == nullptr && (w->g_scales != nullptr || w->bias_g != nullptr)) return MXFP4_ERR_INVALID_ARG;
   return MXFP4_OK;
 }
@@ -93,7 +100,7 @@ mxfp4_status parse_up(const uint8_t* a_codes, const uint8_t* a_scales, const voi
   if (!aligned(plan, 16)) return MXFP4_ERR_UNSUPPORTED;
   const int64_t vs = size_of(w->vec_dtype);
   if (!aligned(w->bias_u, vs) || !aligned(w->bias_g, vs)) return MXFP4_ERR_UNSUPPORTED;
-  set_plan(plan, tokens * topk, experts, f);
+  set_plan(plan, tokens * topk, experts, w->router_experts, f);
   const bool glu = w->g_codes != nullptr;
   const mxfp4_status st = set_operands(a_codes, a_scales, tokens, tokens * topk, w->u_codes, w->u_scales, w->g_codes,
                                        w->g_scales, glu, n, k, layout, f, height);
@@ -201,6 +208,7 @@ MXFP4_API mxfp4_status mxfp4_moe_up(const uint8_t* a_codes, const uint8_t* a_sca
   if (!is_dtype(y_dtype) || !is_layout(layout) || !sizes_ok(tokens, n, k, layout) || ld_y < n) return MXFP4_ERR_INVALID_ARG;
   mxfp4_status st = check_up(w);
   if (st == MXFP4_OK) st = check_plan_sizes(tokens, topk, experts);
+  if (st == MXFP4_OK) st = check_spread(w->router_experts, experts);
   if (st != MXFP4_OK) return st;
   if (tokens == 0 || n == 0) return MXFP4_OK;
   mxfp4::MoeArgs f;
@@ -220,6 +228,7 @@ MXFP4_API mxfp4_status mxfp4_moe_up_requant(const uint8_t* a_codes, const uint8_
   mxfp4_status st = parse_rotation(rot, r);
   if (st == MXFP4_OK) st = check_up(w);
   if (st == MXFP4_OK) st = check_plan_sizes(tokens, topk, experts);
+  if (st == MXFP4_OK) st = check_spread(w->router_experts, experts);
   if (st != MXFP4_OK) return st;
   if (tokens == 0 || n == 0) return MXFP4_OK;
   mxfp4::MoeArgs f;
@@ -238,7 +247,7 @@ MXFP4_API mxfp4_status mxfp4_moe_down_workspace(int64_t tokens, int64_t topk, in
   f.g.m = static_cast<int32_t>(tokens * topk);
   f.g.n = static_cast<int32_t>(n);
   f.g.k = static_cast<int32_t>(k);
-  f.experts = static_cast<int32_t>(experts);
+  f.experts = f.spread = static_cast<int32_t>(experts);
   const int height = mxfp4::moe_tile_rows(f);
   *bytes = tokens == 0 || n == 0 || mxfp4::moe_down_small(f) ? 0 : product_bytes(tokens * topk, n, half_products(f, height, y_dtype));
   return MXFP4_OK;
@@ -250,9 +259,10 @@ MXFP4_API mxfp4_status mxfp4_moe_down(const uint8_t* h_codes, const uint8_t* h_s
                                       const void* residual, int32_t res_dtype, int64_t ld_res, void* y,
                                       int32_t y_dtype, int64_t ld_y, void* workspace, int64_t workspace_bytes,
                                       void* stream) {
-  if (w == nullptr || w->reserved != 0 || !is_dtype(w->vec_dtype) || !is_dtype(res_dtype)) return MXFP4_ERR_INVALID_ARG;
+  if (w == nullptr || !is_dtype(w->vec_dtype) || !is_dtype(res_dtype)) return MXFP4_ERR_INVALID_ARG;
   if (ld_y < n || (residual != nullptr && ld_res < n)) return MXFP4_ERR_INVALID_ARG;
   mxfp4_status st = check_down_sizes(tokens, topk, experts, n, k, layout, y_dtype);
+  if (st == MXFP4_OK) st = check_spread(w->router_experts, experts);
   if (st != MXFP4_OK) return st;
   if (tokens == 0 || n == 0) return MXFP4_OK;
   if (plan == nullptr || weights == nullptr || y == nullptr) return MXFP4_ERR_INVALID_ARG;
@@ -262,7 +272,7 @@ MXFP4_API mxfp4_status mxfp4_moe_down(const uint8_t* h_codes, const uint8_t* h_s
   const int64_t pairs = tokens * topk;
   mxfp4::MoeArgs f;
   int height = 0;
-  set_plan(plan, pairs, experts, f);
+  set_plan(plan, pairs, experts, w->router_experts, f);
   st = set_operands(h_codes, h_scales, pairs, pairs, w->codes, w->scales, nullptr, nullptr, false, n, k, layout, f, height);
   if (st != MXFP4_OK) return st;
   f.vec_bf16 = w->vec_dtype == MXFP4_BF16;

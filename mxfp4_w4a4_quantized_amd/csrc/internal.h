@@ -137,6 +137,7 @@ struct MoeArgs : FusedArgs {
   int32_t a_rows = 0;                 // rows of A
   bool a_tiled = false;               // A's layout (g.tiled: the weights')
   int32_t experts = 0;
+  int32_t spread = 0;                 // experts that the rows are spread over: those, or more on other GPUs
   int64_t w_codes = 0, w_scales = 0;  // bytes from one expert's weights to the next's
   // the result as 16-bit values with a power of two per 32 columns (g.y, z_scales)
   bool z_half = false;

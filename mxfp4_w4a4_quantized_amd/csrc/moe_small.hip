@@ -119,7 +119,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_small_kernel(MoeArgs
 // 1024 17.8 and 10.3.
 // (Below 2^26 columns: a grid holds less than 2^32 threads.)
 bool moe_down_small(const MoeArgs& f) {
-  const int64_t tiles = f.g.m < f.experts ? f.g.m : f.experts;   // at most
+  const int64_t rows = ((int64_t)f.g.m * f.experts + f.spread - 1) / f.spread;   // to expect (all pairs at most: kDownPairs)
+  const int64_t tiles = rows < f.experts ? rows : f.experts;
   return f.g.m <= kDownPairs && f.g.n < (1 << 26) && moe_tile_rows(f) == 16 &&
          (f.g.n >= 12 * cu_count() || tiles * f.g.k <= 32768);
 }

@@ -3,7 +3,10 @@
 
 namespace mxfp4 {
 
-// The height of the row tiles, by the mean number of rows of an expert.
+// The height of the row tiles, by the mean number of rows of an expert: the pairs
+// over all the experts that the router spreads them over, which on one of several
+// GPUs are more than the plan's (64 tokens x 8 of 128, 16 of them here: a mean of 4,
+// not of 32).
 //  * Up to 7 rows 16, up to 18 rows 32: the weights are streamed once or nearly, at 6
 //    to 7.5 TB/s (8 of 128 experts, 4096 -> 2 x 2048, gated; us in tiles of 16, 32 and
 //    128 rows: mean 6 161, 171, 193; 8 169, 166, 189; 12 199, 179, 197; 20 269, 218,
@@ -17,12 +20,13 @@ namespace mxfp4 {
 // same sums.
 int moe_tile_rows(const MoeArgs& f) {
   const GemmArgs& g = f.g;
-  const int64_t mean = g.m / f.experts;
+  const int64_t mean = g.m / f.spread;
   if (mean <= 7) return 16;
   if (mean <= (g.k >= 8192 ? 10 : 18)) return 32;
   if (g.k % large::KS != 0) return 128;
+  const int64_t rows = (int64_t)g.m * f.experts / f.spread;   // to expect
   const int64_t cus = cu_count(), nk = g.k / large::KS, wide = f.glu ? 2 * int64_t(g.n) : g.n;
-  auto tiles = [&](int64_t t) { return (g.m / t + (f.experts + 1) / 2) * ((wide + t - 1) / t); };
+  auto tiles = [&](int64_t t) { return (rows / t + (f.experts + 1) / 2) * ((wide + t - 1) / t); };
   const int64_t t256 = tiles(256), t128 = tiles(128), rest = t128 % (2 * cus);
   const int64_t c256 = (t256 + cus - 1) / cus * (5 * nk + 120);
   const int64_t c128 = t128 / (2 * cus) * (5 * nk + 50) + (rest == 0 ? 0 : (rest <= cus ? 3 * nk : 5 * nk) + 50);

@@ -39,12 +39,16 @@ class RouterDesc(ctypes.Structure):
 class MoeUpDesc(ctypes.Structure):
     _fields_ = ([("act", ctypes.c_int32), ("vec_dtype", ctypes.c_int32)] +
                 [(n, ctypes.c_void_p) for n in ("u_codes", "u_scales", "g_codes", "g_scales", "bias_u", "bias_g")] +
-                [("reserved", ctypes.c_int32)])
+                [("router_experts", ctypes.c_int32)])
 
 
 class MoeDownDesc(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("bias", ctypes.c_void_p),
-                ("vec_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+                ("vec_dtype", ctypes.c_int32), ("router_experts", ctypes.c_int32)]
+
+
+for _desc in (MoeUpDesc, MoeDownDesc):
+    _desc.reserved = _desc.router_experts   # the field's name while it had to be 0
 
 
 def declare(L):
@@ -87,16 +91,19 @@ class ExpertPlan:
     """The pairs (token * topk + choice) in expert order.  offsets [experts + 1]:
     first row of each expert, then the number of rows; order [tokens * topk]: pair
     of each row, -1 behind the last; slot [tokens * topk]: row of each pair, -1
-    where its expert is not among these.  All int32, views of `words`.  Plans come
-    from moe_plan; their sizes do not change."""
+    where its expert is not among these.  All int32, views of `words`.
+    router_experts: those that the pairs are spread over, more than experts where
+    other GPUs hold the rest.  Plans come from moe_plan; their sizes do not change."""
     words: torch.Tensor
     tokens: int
     topk: int
     experts: int
+    router_experts: int
 
-    def __init__(self, words, tokens, topk, experts):
+    def __init__(self, words, tokens, topk, experts, router_experts=None):
         # (a frozen dataclass's own constructor takes 0.4 us more, of a call of 7)
-        self.__dict__.update(words=words, tokens=tokens, topk=topk, experts=experts)
+        self.__dict__.update(words=words, tokens=tokens, topk=topk, experts=experts,
+                             router_experts=experts if router_experts is None else router_experts)
 
     @property
     def offsets(self):
@@ -187,21 +194,26 @@ def _plan_ptr(plan, dev):
     return words.data_ptr()
 
 
-def moe_plan(ids, experts: int, first: int = 0, plan: ExpertPlan = None):
+def moe_plan(ids, experts: int, first: int = 0, plan: ExpertPlan = None, router_experts: int = None):
     """The plan for ids [tokens, topk] (int32) over the experts first .. first +
-    experts - 1; other ids, -1 among them, have no row.  `plan`: one of the same
-    sizes, written again."""
+    experts - 1; other ids, -1 among them, have no row.  router_experts: how many
+    the ids are from, where these are a part of them (the products then choose
+    their kernels by the rows to expect).  `plan`: one of the same sizes, written
+    again."""
     if ids.dim() != 2:
         raise ValueError("ids must be [tokens, topk]")
     dev = _gpu(ids)
     tokens, topk = ids.shape
     ip = _pairs("ids", ids, (tokens, topk), torch.int32, dev)
+    if router_experts is not None and first + experts > router_experts:
+        raise ValueError(f"experts {first} .. {first + experts - 1} are not among {router_experts}")
     if plan is None:
         words = torch.empty_strided((_plan_words(tokens, topk, experts),), (1,), dtype=torch.int32, device=ids.device)
-        plan = ExpertPlan(words, tokens, topk, experts)
-    elif (plan.tokens, plan.topk, plan.experts) != (tokens, topk, experts) or plan.words.get_device() != dev:
-        raise ValueError(f"the plan is for {plan.tokens} tokens, {plan.topk} choices and {plan.experts} experts on "
-                         f"{plan.words.device}")
+        plan = ExpertPlan(words, tokens, topk, experts, router_experts)
+    elif (plan.tokens, plan.topk, plan.experts) != (tokens, topk, experts) or plan.words.get_device() != dev or (
+            router_experts is not None and router_experts != plan.router_experts):
+        raise ValueError(f"the plan is for {plan.tokens} tokens, {plan.topk} choices and {plan.experts} of "
+                         f"{plan.router_experts} experts on {plan.words.device}")
     _check(lib().mxfp4_moe_plan(ip, tokens, topk, first, experts, _plan_ptr(plan, dev), plan.words.numel() * 4,
                                 _stream(dev)), "mxfp4_moe_plan")
     return plan
@@ -253,7 +265,7 @@ def _expert_bias(name, t, experts, n, dtype, dev):
     return t.data_ptr(), t.dtype
 
 
-def _up_desc(act, w_up, w_gate, bias_up, bias_gate, experts, n, k, layout, dev):
+def _up_desc(act, w_up, w_gate, bias_up, bias_gate, experts, router_experts, n, k, layout, dev):
     uc, us = _stack("w_up", *w_up, experts, n, k, layout, dev)
     gc, gs = (None, None) if w_gate is None else _stack("w_gate", *w_gate, experts, n, k, layout, dev)
     bu, bg, dtype = None, None, None
@@ -263,7 +275,7 @@ def _up_desc(act, w_up, w_gate, bias_up, bias_gate, experts, n, k, layout, dev):
         if w_gate is None:
             raise ValueError("bias_gate needs w_gate")
         bg, dtype = _expert_bias("bias_gate", bias_gate, experts, n, dtype, dev)
-    return MoeUpDesc(_act_code(act), 0 if dtype is None else _code(dtype), uc, us, gc, gs, bu, bg, 0)
+    return MoeUpDesc(_act_code(act), 0 if dtype is None else _code(dtype), uc, us, gc, gs, bu, bg, router_experts)
 
 
 def _width(weight, layout, n, name="n"):
@@ -279,7 +291,7 @@ def moe_up(a_codes, a_scales, plan: ExpertPlan, w_up, w_gate=None, act="silu", b
     dev = _gpu(a_codes)
     n, k = _width(w_up[0], layout, n), a_codes.shape[1] * 2
     ac, as_ = _packed("activations", a_codes, a_scales, plan.tokens, k, layout, dev)
-    desc = _up_desc(act, w_up, w_gate, bias_up, bias_gate, plan.experts, n, k, layout, dev)
+    desc = _up_desc(act, w_up, w_gate, bias_up, bias_gate, plan.experts, plan.router_experts, n, k, layout, dev)
     y, ptr, ld, yt = _dense_output(y, plan.tokens * plan.topk, n, out_dtype, a_codes)
     _check(lib().mxfp4_moe_up(ac, as_, _plan_ptr(plan, dev), plan.tokens, plan.topk, plan.experts, desc, n, k, layout, ptr,
                               yt, ld, _stream(dev)), "mxfp4_moe_up")
@@ -293,7 +305,7 @@ def moe_up_requant(a_codes, a_scales, plan: ExpertPlan, w_up, w_gate=None, act="
     dev = _gpu(a_codes)
     n, k = _width(w_up[0], layout, n), a_codes.shape[1] * 2
     ac, as_ = _packed("activations", a_codes, a_scales, plan.tokens, k, layout, dev)
-    desc = _up_desc(act, w_up, w_gate, bias_up, bias_gate, plan.experts, n, k, layout, dev)
+    desc = _up_desc(act, w_up, w_gate, bias_up, bias_gate, plan.experts, plan.router_experts, n, k, layout, dev)
     rdesc, _keep = _rotation(rot, a_codes, n)
     y_codes, y_scales, yc, ys = _packed_outputs(plan.tokens * plan.topk, n, out_layout, y_codes, y_scales, a_codes)
     _check(lib().mxfp4_moe_up_requant(ac, as_, _plan_ptr(plan, dev), plan.tokens, plan.topk, plan.experts, desc, n, k,
@@ -302,10 +314,10 @@ def moe_up_requant(a_codes, a_scales, plan: ExpertPlan, w_up, w_gate=None, act="
 
 
 @functools.lru_cache(maxsize=4096)
-def _down_workspace(tokens, topk, experts, n, k, layout, yt, dev):
+def _down_workspace(tokens, topk, router_experts, n, k, layout, yt, dev):
     """Bytes of the workspace on GPU dev (the current one)."""
     b = ctypes.c_int64()
-    _check(lib().mxfp4_moe_down_workspace(tokens, topk, experts, n, k, layout, yt, ctypes.byref(b)),
+    _check(lib().mxfp4_moe_down_workspace(tokens, topk, router_experts, n, k, layout, yt, ctypes.byref(b)),
            "mxfp4_moe_down_workspace")
     return b.value
 
@@ -331,10 +343,10 @@ def moe_down(h_codes, h_scales, plan: ExpertPlan, weights, w_down, bias=None, re
     wp = _pairs("weights", weights, (plan.tokens, plan.topk), torch.float32, dev)
     dc, ds = _stack("w_down", *w_down, plan.experts, n, k, layout, dev)
     bp, bt = (None, None) if bias is None else _expert_bias("bias", bias, plan.experts, n, None, dev)
-    desc = MoeDownDesc(dc, ds, bp, 0 if bt is None else _code(bt), 0)
+    desc = MoeDownDesc(dc, ds, bp, 0 if bt is None else _code(bt), plan.router_experts)
     res, rt, ld_r = _residual(residual, (plan.tokens, n), dev)
     y, ptr, ld, yt = _dense_output(y, plan.tokens, n, out_dtype, h_codes)
-    need = _down_workspace(plan.tokens, plan.topk, plan.experts, n, k, layout, yt, dev)
+    need = _down_workspace(plan.tokens, plan.topk, plan.router_experts, n, k, layout, yt, dev)
     wsp, size = None, 0
     if workspace is None:
         if need > 0:
@@ -352,18 +364,18 @@ def moe_down(h_codes, h_scales, plan: ExpertPlan, weights, w_down, bias=None, re
 
 def moe_down_workspace(plan: ExpertPlan, n: int, k: int, out_dtype=torch.bfloat16, layout: int = ROWMAJOR):
     """Bytes of moe_down's workspace for hidden activations of width k."""
-    return _down_workspace(plan.tokens, plan.topk, plan.experts, n, k, layout, _code(out_dtype), _gpu(plan.words))
+    return _down_workspace(plan.tokens, plan.topk, plan.router_experts, n, k, layout, _code(out_dtype), _gpu(plan.words))
 
 
 @functools.lru_cache(maxsize=4096)
-def _ffn_work(tokens, topk, experts, d, hidden, layout, yt, dev):
+def _ffn_work(tokens, topk, experts, router_experts, d, hidden, layout, yt, dev):
     """Offsets of what lies between moe_ffn's calls in its allocation (ids, weights,
     plan, codes and scales of x and of the hidden activations, workspace), the
     allocation's size, and the plan's and the workspace's."""
     rows = tokens * topk
     tp, rp = (padded_rows(tokens), padded_rows(rows)) if layout == TILED else (tokens, rows)
     plan = 4 * _plan_words(tokens, topk, experts)
-    work = _down_workspace(tokens, topk, experts, d, hidden, layout, yt, dev)
+    work = _down_workspace(tokens, topk, router_experts, d, hidden, layout, yt, dev)
     starts, total = [], 0
     for size in (rows * 4, rows * 4, plan, tp * d // 2, tp * d // 32, rp * hidden // 2, rp * hidden // 32, work):
         starts.append(total)
@@ -402,17 +414,17 @@ def moe_ffn(x, logits, r: Router, w_up, w_down, hidden: int, w_gate=None, act="s
     lp, ld_l = _matrix("logits", logits, logits.shape, dev)
     router = _router_desc(r, logits.shape[1], dev)
     rdesc = None if rot is None else _H32
-    up = _up_desc(act, w_up, w_gate, bias_up, bias_gate, experts, hidden, d, layout, dev)
+    up = _up_desc(act, w_up, w_gate, bias_up, bias_gate, experts, logits.shape[1], hidden, d, layout, dev)
     dc, ds = _stack("w_down", *w_down, experts, d, hidden, layout, dev)
     bp, bt = (None, None) if bias_down is None else _expert_bias("bias_down", bias_down, experts, d, None, dev)
-    down = MoeDownDesc(dc, ds, bp, 0 if bt is None else _code(bt), 0)
+    down = MoeDownDesc(dc, ds, bp, 0 if bt is None else _code(bt), logits.shape[1])
     res, rt, ld_r = _residual(residual, x.shape, dev)
     if out_dtype is None:
         out_dtype = x.dtype if residual is None else residual.dtype
     y, yp, ld_y, yt = _dense_output(y, tokens, d, out_dtype, x)
     if tokens == 0:
         return y
-    starts, total, plan_size, work_size = _ffn_work(tokens, topk, experts, d, hidden, layout, yt, dev)
+    starts, total, plan_size, work_size = _ffn_work(tokens, topk, experts, logits.shape[1], d, hidden, layout, yt, dev)
     work = torch.empty_strided((total,), (1,), dtype=torch.uint8, device=x.device)
     base = work.data_ptr()
     ids, weights, plan, ac, as_, hc, hs, ws = [base + at for at in starts]

@@ -1,4 +1,5 @@
 """What the mixture-of-experts binding refuses by sizes alone, on the CPU."""
+import ctypes
 import dataclasses
 
 import pytest
@@ -41,3 +42,30 @@ def test_products_refuse_a_plan_whose_words_are_not_of_its_sizes():
         moe._plan_ptr(mx.ExpertPlan(words, 10, 3, 5), 0)
     with pytest.raises(dataclasses.FrozenInstanceError):
         mx.ExpertPlan(words, 10, 3, 5).topk = 30
+
+
+A = 1 << 20          # an aligned address, never dereferenced
+INV, UNS, OK = mx.MXFP4_ERR_INVALID_ARG, mx.MXFP4_ERR_UNSUPPORTED, mx.MXFP4_OK
+
+
+@pytest.mark.parametrize("of,want", [(0, OK), (8, OK), (9, OK), (1024, OK), (7, INV), (1, INV), (-1, INV), (1025, UNS)])
+def test_router_experts_are_at_least_the_plans(of, want):
+    """(no columns: nothing is launched)"""
+    up = moe.MoeUpDesc(2, 0, A, A, None, None, None, None, of)
+    down = moe.MoeDownDesc(A, A, None, 0, of)
+    L = mx.lib()
+    assert L.mxfp4_moe_up(A, A, A, 4, 2, 8, up, 0, 128, 0, A, 0, 0, None) == want
+    assert L.mxfp4_moe_up_requant(A, A, A, 4, 2, 8, up, 0, 128, 0, None, A, A, 0, None) == want
+    assert L.mxfp4_moe_down(A, A, A, 4, 2, 8, A, down, 0, 128, 0, None, 0, 0, A, 0, 0, None, 0, None) == want
+
+
+def test_workspace_of_a_part_of_the_experts():
+    """64 tokens x 8 of 128 experts, 16 of them here: a mean of 4 rows, whose products
+    are fp32; as if all pairs went to the 16 (32 rows) they would be held in 16 bits."""
+    def need(plan, n):
+        b = ctypes.c_int64()
+        assert mx.lib().mxfp4_moe_down_workspace(plan.tokens, plan.topk, plan.router_experts, n, 2048, 0, mx.MXFP4_BF16,
+                                                 ctypes.byref(b)) == OK
+        return b.value
+    assert need(mx.ExpertPlan(None, 64, 8, 16, 128), 4096) >= 512 * 4096 * 4
+    assert need(mx.ExpertPlan(None, 64, 8, 16), 4096) < 512 * 4096 * 4
