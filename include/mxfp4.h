@@ -648,7 +648,8 @@ typedef struct {
  *                     With router_experts, mxfp4_moe_down_workspace is asked with
  *                     that number as its experts
  * Errors: as mxfp4_moe_up (null weights are INVALID_ARG, and so is a workspace
- *   that is missing or too short). */
+ *   that is missing or too short).  Sizes that mxfp4_moe_down refuses are refused
+ *   by mxfp4_moe_down_workspace too. */
 MXFP4_API mxfp4_status mxfp4_moe_down_workspace(int64_t tokens, int64_t topk, int64_t experts, int64_t n, int64_t k,
                                                 int32_t layout, int32_t y_dtype, int64_t* bytes);
 MXFP4_API mxfp4_status mxfp4_moe_down(const uint8_t* h_codes, const uint8_t* h_scales, const void* plan,

@@ -39,6 +39,18 @@ void set_plan(const void* plan, int64_t pairs, int64_t experts, int32_t router_e
   f.spread = router_experts != 0 ? router_experts : f.experts;
 }
 
+// What the tile kernels hold of sizes: 32-bit offsets within A (`rows` rows) and
+// within one expert's weights, 32-bit tile numbers.
+mxfp4_status check_limits(int64_t rows, int64_t pairs, int64_t experts, int64_t n, int64_t k, int height) {
+  if (height < 128) return MXFP4_OK;
+  const int64_t arows = (rows + mxfp4::kTileRows - 1) / mxfp4::kTileRows * mxfp4::kTileRows;
+  const int64_t limit = int64_t(1) << 32, tiles_n = (n + 63) / 64;
+  if (arows * (k / 2) >= limit || (n + 255) / 256 * 256 * (k / 2) >= limit ||
+      mxfp4::moe::max_tiles(pairs, experts, height) * tiles_n >= (int64_t(1) << 31))
+    return MXFP4_ERR_UNSUPPORTED;
+  return MXFP4_OK;
+}
+
 // Operands of a product: `rows` rows of A, `pairs` of the result, experts' weights
 // of n x k.  Then the kernel: its row tiles' height.
 mxfp4_status set_operands(const uint8_t* a_codes, const uint8_t* a_scales, int64_t rows, int64_t pairs,
@@ -70,15 +82,7 @@ mxfp4_status set_operands(const uint8_t* a_codes, const uint8_t* a_scales, int64
   f.w_codes = wrows * (k / 2);
   f.w_scales = wrows * (k / 32);
   height = mxfp4::moe_tile_rows(f);
-  if (height >= 128) {
-    // 32-bit offsets within A and within one expert's weights, 32-bit tile numbers
-    const int64_t arows = (rows + mxfp4::kTileRows - 1) / mxfp4::kTileRows * mxfp4::kTileRows;
-    const int64_t limit = int64_t(1) << 32, tiles_n = (n + 63) / 64;
-    if (arows * (k / 2) >= limit || (n + 255) / 256 * 256 * (k / 2) >= limit ||
-        mxfp4::moe::max_tiles(pairs, f.experts, height) * tiles_n >= (int64_t(1) << 31))
-      return MXFP4_ERR_UNSUPPORTED;
-  }
-  return MXFP4_OK;
+  return check_limits(rows, pairs, f.experts, n, k, height);
 }
 
 mxfp4_status launch(const mxfp4::MoeArgs& f, int height, void* stream) {
@@ -241,7 +245,7 @@ MXFP4_API mxfp4_status mxfp4_moe_up_requant(const uint8_t* a_codes, const uint8_
 MXFP4_API mxfp4_status mxfp4_moe_down_workspace(int64_t tokens, int64_t topk, int64_t experts, int64_t n, int64_t k,
                                                 int32_t layout, int32_t y_dtype, int64_t* bytes) {
   if (bytes == nullptr) return MXFP4_ERR_INVALID_ARG;
-  const mxfp4_status st = check_down_sizes(tokens, topk, experts, n, k, layout, y_dtype);
+  mxfp4_status st = check_down_sizes(tokens, topk, experts, n, k, layout, y_dtype);
   if (st != MXFP4_OK) return st;
   mxfp4::MoeArgs f;
   f.g.m = static_cast<int32_t>(tokens * topk);
@@ -249,6 +253,8 @@ MXFP4_API mxfp4_status mxfp4_moe_down_workspace(int64_t tokens, int64_t topk, in
   f.g.k = static_cast<int32_t>(k);
   f.experts = f.spread = static_cast<int32_t>(experts);
   const int height = mxfp4::moe_tile_rows(f);
+  if (tokens > 0 && n > 0) st = check_limits(tokens * topk, tokens * topk, experts, n, k, height);
+  if (st != MXFP4_OK) return st;
   *bytes = tokens == 0 || n == 0 || mxfp4::moe_down_small(f) ? 0 : product_bytes(tokens * topk, n, half_products(f, height, y_dtype));
   return MXFP4_OK;
 }

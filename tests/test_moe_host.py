@@ -69,3 +69,17 @@ def test_workspace_of_a_part_of_the_experts():
         return b.value
     assert need(mx.ExpertPlan(None, 64, 8, 16, 128), 4096) >= 512 * 4096 * 4
     assert need(mx.ExpertPlan(None, 64, 8, 16), 4096) < 512 * 4096 * 4
+
+
+@pytest.mark.parametrize("tokens,topk,experts,n,k", [(75000, 8, 64, 4096, 14336), (1 << 21, 1, 1, 128, 1 << 13),
+                                                     (1 << 12, 1, 1, 1 << 26, 128), (4096, 2, 8, 128, 1 << 26)])
+def test_workspace_refuses_what_the_product_refuses(tokens, topk, experts, n, k):
+    """Code bytes of A or of one expert past 2^32: known before anything is launched."""
+    b = ctypes.c_int64()
+    w = moe.MoeDownDesc(A, A, None, 0, 0)
+    for layout in (0, 1):
+        assert mx.lib().mxfp4_moe_down(A, A, A, tokens, topk, experts, A, w, n, k, layout, None, 0, 0, A, 0, n, A, 1 << 60,
+                                       None) == UNS
+        assert mx.lib().mxfp4_moe_down_workspace(tokens, topk, experts, n, k, layout, 0, ctypes.byref(b)) == UNS
+    with pytest.raises(mx.Mxfp4Error):                                # moe_ffn's sizes of the same block
+        moe._ffn_work(tokens, topk, experts, experts, n, k, mx.TILED, mx.MXFP4_F32, -1)
