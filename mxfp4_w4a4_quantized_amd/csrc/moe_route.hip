@@ -645,10 +645,14 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(CombineArgs a) {
 
 hipError_t launch_moe_route(const RouteArgs& a, hipStream_t s) {
   const int e = a.experts;
-  // (4096 tokens, sigmoid, bias, 8 groups: 64 experts 6.6 us on 16 lanes, 7.8 on 64;
-  // 2048 tokens 6.5 and 6.1; 6000 tokens,
-  // 256 experts 13.3 on 32, 14.8 on 64)
-  if (a.tokens >= 3000 && e <= 256 && a.topk <= 16) {
+  // Lanes a token, and us on that many and on 64 (topk 8; softmax / sigmoid with a
+  // bias and 8 groups):
+  //   64 experts, 16 lanes:  2048 tokens 4.3, 4.3 / 6.5, 6.2;  3000 4.3, 5.0 / 6.5, 7.0
+  //   128 experts, 16 lanes: 3000 tokens 5.5, 5.6 / 8.8, 8.0;  4096 5.6, 6.4 / 8.9, 9.1;  8192 6.2, 9.7 / 10.3, 14.0
+  //   256 experts, 32 lanes: 3000 tokens 6.7, 6.5 / 11.1, 9.8; 4096 6.7, 7.4 / 11.3, 11.3; 8192 8.9, 11.2 / 15.6, 17.8
+  // Of more experts 32 lanes have no such crossing (512 experts, 8192 tokens: 13.3, 14.8 /
+  // 28.8, 26.9); fewer lanes than 64 hold at most 16 choices here.
+  if (a.tokens >= (e <= 64 ? 3000 : 4096) && e <= 256 && a.topk <= 16) {
     if (e <= 64) launch_route_nv<16, 4>(a, s);
     else if (e <= 128) launch_route_nv<16, 8>(a, s);
     else launch_route_nv<32, 8>(a, s);
