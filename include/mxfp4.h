@@ -526,9 +526,12 @@ typedef enum {
  * group score (of s + bias, or of s without a bias) are kept, the others left
  * out.  Then the topk largest keys, in descending order, ties to the lowest
  * index, between groups too.  weights = s of the chosen, divided by their sum if
- * renormalize (0 where that sum is 0), times scale.  Scores, keys with a bias and
- * group scores are formed in binary64 (two s + bias that agree to 2^-42 of their
- * value count as equal), weights rounded once.
+ * renormalize (0 where that sum is 0), times scale.  All of it is formed in
+ * binary64, weights rounded once.  What that is worth: e^x is right to 2^-47 of its
+ * value (from 2^-1022 down to its subnormal steps, 2^-1074), a sigmoid to 2^-45; a
+ * key with a bias and the keys that a group's score is made of keep 42 bits, so two
+ * s + bias that agree to 2^-42 of their value may count as equal.  Keys without a
+ * bias are the logits, exactly.
  * Logits of -infinity or NaN are experts that cannot be chosen; a bias of
  * -infinity or NaN takes one out as well.  Where fewer than topk can be chosen,
  * the remaining ids are -1 with weight 0.  A logit of +infinity makes a token's

@@ -121,8 +121,9 @@ __device__ __forceinline__ T across(T v, Op op) {
 }
 
 // e^x in 64 bits, relative error some 2^-47: x = n ln 2 + r, |r| <= ln 2 / 2, with
-// ln 2 in two parts (Cody and Waite), and the series of e^r to r^11.  0 below -700.
-// N values step by step together: one alone waits for each of its operations.
+// ln 2 in two parts (Cody and Waite), and the series of e^r to r^11; below 2^-1022
+// in binary64's subnormal steps.  N values step by step together: one alone waits
+// for each of its operations.
 template <int N>
 __device__ __forceinline__ void exp64(double (&x)[N]) {
   constexpr double kSeries[] = {1.0 / 39916800, 1.0 / 3628800, 1.0 / 362880, 1.0 / 40320, 1.0 / 5040, 1.0 / 720,
@@ -143,10 +144,8 @@ __device__ __forceinline__ void exp64(double (&x)[N]) {
     __builtin_amdgcn_sched_barrier(0);
   }
 #pragma unroll
-  for (int i = 0; i < N; ++i) {   // p 2^n by its exponent field
-    const uint64_t e = __builtin_bit_cast(uint64_t, p[i]) + (__builtin_bit_cast(uint64_t, big[i]) << 52);
-    x[i] = x[i] < -700.0 ? 0.0 : __builtin_bit_cast(double, e);
-  }
+  for (int i = 0; i < N; ++i)   // (far below, n's lowest bits are not n; x = -infinity)
+    x[i] = x[i] < -746.0 ? 0.0 : __builtin_ldexp(p[i], (int)(uint32_t)__builtin_bit_cast(uint64_t, big[i]));
 }
 // 1 / (1 + e^-x).  v_rcp_f64 is right to some 2^-23, a Newton step makes that 2^-45,
 // beyond what a key keeps.
