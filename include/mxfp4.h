@@ -608,8 +608,9 @@ typedef struct {
  * Errors: INVALID_ARG as mxfp4_gemm_glu, for a null plan, and for a gate's
  *   scales or bias without its codes; UNSUPPORTED for misaligned pointers (codes
  *   and plan 16 bytes, scales 4 where k is a multiple of 128, biases and y their
- *   elements), n or k >= 2^30, code bytes of A or of one expert past 2^32, and
- *   the limits above; HIP if the launch fails. */
+ *   elements), n or k >= 2^30, code bytes of A or of one expert past 2^32 where
+ *   an expert has more than 18 rows in the mean, and the limits above; HIP if
+ *   the launch fails. */
 MXFP4_API mxfp4_status mxfp4_moe_up(const uint8_t* a_codes, const uint8_t* a_scales, const void* plan,
                                     int64_t tokens, int64_t topk, int64_t experts,
                                     const mxfp4_moe_up_weights* w, int64_t n, int64_t k, int32_t layout, void* y,

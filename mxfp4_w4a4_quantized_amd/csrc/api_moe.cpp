@@ -39,16 +39,19 @@ void set_plan(const void* plan, int64_t pairs, int64_t experts, int32_t router_e
   f.spread = router_experts != 0 ? router_experts : f.experts;
 }
 
-// What the tile kernels hold of sizes: 32-bit offsets within A (`rows` rows) and
-// within one expert's weights, 32-bit tile numbers.
-mxfp4_status check_limits(int64_t rows, int64_t pairs, int64_t experts, int64_t n, int64_t k, int height) {
+// The height of a product's row tiles.  The tile kernels hold 32-bit offsets within A
+// (`rows` rows) and within one expert's weights, and 32-bit tile numbers: past those
+// few rows an expert go in tiles of 16, many are refused.
+mxfp4_status choose_height(const mxfp4::MoeArgs& f, int64_t rows, int& height) {
+  height = mxfp4::moe_tile_rows(f);
   if (height < 128) return MXFP4_OK;
-  const int64_t arows = (rows + mxfp4::kTileRows - 1) / mxfp4::kTileRows * mxfp4::kTileRows;
+  const int64_t n = f.g.n, k = f.g.k, arows = (rows + mxfp4::kTileRows - 1) / mxfp4::kTileRows * mxfp4::kTileRows;
   const int64_t limit = int64_t(1) << 32, tiles_n = (n + 63) / 64;
-  if (arows * (k / 2) >= limit || (n + 255) / 256 * 256 * (k / 2) >= limit ||
-      mxfp4::moe::max_tiles(pairs, experts, height) * tiles_n >= (int64_t(1) << 31))
-    return MXFP4_ERR_UNSUPPORTED;
-  return MXFP4_OK;
+  if (arows * (k / 2) < limit && (n + 255) / 256 * 256 * (k / 2) < limit &&
+      mxfp4::moe::max_tiles(f.g.m, f.experts, height) * tiles_n < (int64_t(1) << 31))
+    return MXFP4_OK;
+  height = 16;
+  return f.g.m / f.spread <= 18 ? MXFP4_OK : MXFP4_ERR_UNSUPPORTED;
 }
 
 // Operands of a product: `rows` rows of A, `pairs` of the result, experts' weights
@@ -81,8 +84,7 @@ mxfp4_status set_operands(const uint8_t* a_codes, const uint8_t* a_scales, int64
   f.a_tiled = tiled;
   f.w_codes = wrows * (k / 2);
   f.w_scales = wrows * (k / 32);
-  height = mxfp4::moe_tile_rows(f);
-  return check_limits(rows, pairs, f.experts, n, k, height);
+  return choose_height(f, rows, height);
 }
 
 mxfp4_status launch(const mxfp4::MoeArgs& f, int height, void* stream) {
@@ -252,8 +254,9 @@ MXFP4_API mxfp4_status mxfp4_moe_down_workspace(int64_t tokens, int64_t topk, in
   f.g.n = static_cast<int32_t>(n);
   f.g.k = static_cast<int32_t>(k);
   f.experts = f.spread = static_cast<int32_t>(experts);
-  const int height = mxfp4::moe_tile_rows(f);
-  if (tokens > 0 && n > 0) st = check_limits(tokens * topk, tokens * topk, experts, n, k, height);
+  f.g.tiled = layout == MXFP4_LAYOUT_TILED;
+  int height = 0;
+  if (tokens > 0 && n > 0) st = choose_height(f, f.g.m, height);
   if (st != MXFP4_OK) return st;
   *bytes = tokens == 0 || n == 0 || mxfp4::moe_down_small(f) ? 0 : product_bytes(tokens * topk, n, half_products(f, height, y_dtype));
   return MXFP4_OK;

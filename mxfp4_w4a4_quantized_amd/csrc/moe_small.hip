@@ -22,8 +22,10 @@ void launch_layout(const MoeArgs& f, hipStream_t s) {
 
 template <int MG, int PG, int OUT, bool GLU>
 void launch(const MoeArgs& f, hipStream_t s) {
-  if (f.g.tiled) launch_layout<MG, PG, OUT, GLU, true>(f, s);
-  else launch_layout<MG, PG, OUT, GLU, false>(f, s);
+  if constexpr (MG == 1) {
+    if (!f.g.tiled) return launch_layout<MG, PG, OUT, GLU, false>(f, s);
+  }
+  launch_layout<MG, PG, OUT, GLU, true>(f, s);   // (rows of 32 are for tiled operands only: moe_tile_rows)
 }
 
 template <int MG>
@@ -113,15 +115,15 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_small_kernel(MoeArgs
 
 }  // namespace
 
-// Few pairs (of more, the second launch is a small part), and columns for most CUs or
-// little for each workgroup to read: 4 x 4 of 32, 1024 -> 1024 5.5 us against 5.9 in
-// two launches, 12 x 3 of 10, 2816 -> 2816 11.3 and 13.2, but 16 x 8 of 32, 2048 ->
-// 1024 17.8 and 10.3.
-// (Below 2^26 columns: a grid holds less than 2^32 threads.)
+// Few pairs (of more, the second launch is a small part) of few rows an expert, and
+// columns for most CUs or little for each workgroup to read: 4 x 4 of 32, 1024 -> 1024
+// 5.5 us against 5.9 in two launches, 12 x 3 of 10, 2816 -> 2816 11.3 and 13.2, but 16 x
+// 8 of 32, 2048 -> 1024 17.8 and 10.3.  (Below 2^26 columns: a grid holds less than 2^32
+// threads.)
 bool moe_down_small(const MoeArgs& f) {
   const int64_t rows = ((int64_t)f.g.m * f.experts + f.spread - 1) / f.spread;   // to expect (all pairs at most: kDownPairs)
   const int64_t tiles = rows < f.experts ? rows : f.experts;
-  return f.g.m <= kDownPairs && f.g.n < (1 << 26) && moe_tile_rows(f) == 16 &&
+  return f.g.m <= kDownPairs && f.g.n < (1 << 26) && f.g.m / f.spread <= 7 &&
          (f.g.n >= 12 * cu_count() || tiles * f.g.k <= 32768);
 }
 

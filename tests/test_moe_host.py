@@ -64,7 +64,7 @@ def test_workspace_of_a_part_of_the_experts():
     are fp32; as if all pairs went to the 16 (32 rows) they would be held in 16 bits."""
     def need(plan, n):
         b = ctypes.c_int64()
-        assert mx.lib().mxfp4_moe_down_workspace(plan.tokens, plan.topk, plan.router_experts, n, 2048, 0, mx.MXFP4_BF16,
+        assert mx.lib().mxfp4_moe_down_workspace(plan.tokens, plan.topk, plan.router_experts, n, 2048, 1, mx.MXFP4_BF16,
                                                  ctypes.byref(b)) == OK
         return b.value
     assert need(mx.ExpertPlan(None, 64, 8, 16, 128), 4096) >= 512 * 4096 * 4
