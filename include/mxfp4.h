@@ -645,7 +645,10 @@ typedef struct {
  *   y                 device [tokens][ld_y] of y_dtype.  Sums in fp32, in the order
  *                     of a token's choices, the residual first.  For a bf16 y the
  *                     single products may be held in 16 bits, 11 of them
- *                     significant: an eighth of bf16's rounding
+ *                     significant, down to 2^-28 of the largest of their 32
+ *                     columns: each is off by 2^-12 of itself, an eighth of bf16's
+ *                     own rounding (against the products, not against a sum in
+ *                     which they cancel).  Products of an fp32 y are fp32
  *   workspace         device, 256-byte aligned, of mxfp4_moe_down_workspace bytes
  *                     (the products; 0 for few pairs: then it may be NULL); needs
  *                     no clearing, and calls that may overlap in time need one each.

@@ -777,7 +777,11 @@ __global__ __launch_bounds__(T::NT, T::WGS) void gemm_fused_large_kernel(Args f,
           take(o, bb, v);
           if constexpr (OUT == 3) {
             // 2^14 <= amax < 2^15 after scaling: no overflow, and 11 bits for every
-            // value down to 2^-29 of the block's largest (the exponent stays in 1 .. 254)
+            // value down to 2^-28 of the block's largest (the smallest normal number is
+            // 2^-14; the exponent stays in 1 .. 254).  A choice, for half the bytes (8192 x
+            // 8 of 64, 2048 -> 4096: 510 us a call, 663 with fp32 products): each product is
+            // off by 2^-12 of itself, an eighth of the bf16 result's own rounding; where a
+            // token's products cancel it counts against them, not against their sum.
             float am = 0.0f;
 #pragma unroll
             for (int r = 0; r < 16; ++r) am = fmaxf(am, fabsf(v[r]));

@@ -278,18 +278,21 @@ def _up_desc(act, w_up, w_gate, bias_up, bias_gate, experts, router_experts, n, 
     return MoeUpDesc(_act_code(act), 0 if dtype is None else _code(dtype), uc, us, gc, gs, bu, bg, router_experts)
 
 
-def _width(weight, layout, n, name="n"):
-    """Rows of one expert's weight: given, where TILED pads them."""
-    return weight.shape[1] if n is None else n
+def _width(codes, n):
+    """Rows of one expert's weight: n, or all that the stack holds (TILED: the
+    padding too)."""
+    return codes.shape[1] if n is None else n
 
 
 def moe_up(a_codes, a_scales, plan: ExpertPlan, w_up, w_gate=None, act="silu", bias_up=None, bias_gate=None,
            out_dtype=torch.bfloat16, y=None, layout: int = ROWMAJOR, n: int = None):
     """H [tokens * topk, n], row p for row p of the plan (rows behind its last are
     not written).  a: the tokens' packed activations; w_up, w_gate: (codes, scales)
-    stacks; bias_up, bias_gate: [experts, n]."""
+    stacks; bias_up, bias_gate: [experts, n].  n: rows of one expert's weight, by
+    default all that its stack holds (for TILED weights the padding too: give n
+    where it is no multiple of 256)."""
     dev = _gpu(a_codes)
-    n, k = _width(w_up[0], layout, n), a_codes.shape[1] * 2
+    n, k = _width(w_up[0], n), a_codes.shape[1] * 2
     ac, as_ = _packed("activations", a_codes, a_scales, plan.tokens, k, layout, dev)
     desc = _up_desc(act, w_up, w_gate, bias_up, bias_gate, plan.experts, plan.router_experts, n, k, layout, dev)
     y, ptr, ld, yt = _dense_output(y, plan.tokens * plan.topk, n, out_dtype, a_codes)
@@ -301,9 +304,10 @@ def moe_up(a_codes, a_scales, plan: ExpertPlan, w_up, w_gate=None, act="silu", b
 def moe_up_requant(a_codes, a_scales, plan: ExpertPlan, w_up, w_gate=None, act="silu", bias_up=None, bias_gate=None,
                    rot=None, layout: int = ROWMAJOR, out_layout: int = ROWMAJOR, n: int = None, y_codes=None,
                    y_scales=None):
-    """(codes, scales) of rot(H), H as moe_up gives it in fp32; rot None or "h32"."""
+    """(codes, scales) of rot(H), H as moe_up gives it in fp32 (n as there); rot None
+    or "h32"."""
     dev = _gpu(a_codes)
-    n, k = _width(w_up[0], layout, n), a_codes.shape[1] * 2
+    n, k = _width(w_up[0], n), a_codes.shape[1] * 2
     ac, as_ = _packed("activations", a_codes, a_scales, plan.tokens, k, layout, dev)
     desc = _up_desc(act, w_up, w_gate, bias_up, bias_gate, plan.experts, plan.router_experts, n, k, layout, dev)
     rdesc, _keep = _rotation(rot, a_codes, n)
@@ -334,10 +338,11 @@ def moe_down(h_codes, h_scales, plan: ExpertPlan, weights, w_down, bias=None, re
              y=None, layout: int = ROWMAJOR, n: int = None, workspace=None):
     """y [tokens, n] = residual + sum over a token's choices of weight * (h D_e^T +
     bias).  h: packed activations of tokens * topk rows, in the plan's order;
-    weights: [tokens, topk] fp32; bias: [experts, n]; residual may be y itself;
-    workspace: uint8, of moe_down_workspace bytes (a new one if not given)."""
+    weights: [tokens, topk] fp32; bias: [experts, n]; residual may be y itself; n as
+    in moe_up; workspace: uint8, of moe_down_workspace bytes (a new one if not given).
+    A bf16 y may come from products held in 11 bits each; an fp32 one never does."""
     dev = _gpu(h_codes)
-    n, k = _width(w_down[0], layout, n), h_codes.shape[1] * 2
+    n, k = _width(w_down[0], n), h_codes.shape[1] * 2
     rows = plan.tokens * plan.topk
     hc, hs = _packed("hidden activations", h_codes, h_scales, rows, k, layout, dev)
     wp = _pairs("weights", weights, (plan.tokens, plan.topk), torch.float32, dev)
