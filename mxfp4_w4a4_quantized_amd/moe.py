@@ -188,7 +188,7 @@ def _plan_ptr(plan, dev):
     if words.get_device() != dev:
         raise _bad("the plan", words, words.shape, dev)
     need = _plan_words(plan.tokens, plan.topk, plan.experts)
-    if words.dtype != torch.int32 or words.shape != (need,) or not words.is_contiguous():
+    if words.numel() != need or words.dtype != torch.int32 or words.dim() != 1 or not words.is_contiguous():
         raise ValueError(f"a plan of {plan.tokens} tokens, {plan.topk} choices and {plan.experts} experts has {need} "
                          f"contiguous int32 words, got {words.dtype} {tuple(words.shape)}")
     return words.data_ptr()
@@ -210,12 +210,15 @@ def moe_plan(ids, experts: int, first: int = 0, plan: ExpertPlan = None, router_
     if plan is None:
         words = torch.empty_strided((_plan_words(tokens, topk, experts),), (1,), dtype=torch.int32, device=ids.device)
         plan = ExpertPlan(words, tokens, topk, experts, router_experts)
+        ptr = words.data_ptr()
     elif (plan.tokens, plan.topk, plan.experts) != (tokens, topk, experts) or plan.words.get_device() != dev or (
             router_experts is not None and router_experts != plan.router_experts):
         raise ValueError(f"the plan is for {plan.tokens} tokens, {plan.topk} choices and {plan.experts} of "
                          f"{plan.router_experts} experts on {plan.words.device}")
-    _check(lib().mxfp4_moe_plan(ip, tokens, topk, first, experts, _plan_ptr(plan, dev), plan.words.numel() * 4,
-                                _stream(dev)), "mxfp4_moe_plan")
+    else:
+        ptr = _plan_ptr(plan, dev)
+    _check(lib().mxfp4_moe_plan(ip, tokens, topk, first, experts, ptr, plan.words.numel() * 4, _stream(dev)),
+           "mxfp4_moe_plan")
     return plan
 
 
