@@ -1,5 +1,5 @@
-"""Mixture-of-experts calls of more tokens or columns than one grid's 2^32 threads
-hold.  Whole batches are compared on the device, or their rows with those of
+"""Mixture-of-experts calls at the largest numbers of choices and experts, and of more
+tokens or columns than one grid's 2^32 threads hold.  Whole batches are compared on the device, or their rows with those of
 short calls on a part of the same logits."""
 import ctypes
 
@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import mxfp4_w4a4_quantized_amd as mx
+import test_gpu_moe as products
 
 pytestmark = pytest.mark.gpu
 
@@ -91,3 +92,11 @@ def test_route_past_one_grid_64_lanes():
         part, pw = mx.moe_route(logits[at:at + 2500], r)
         assert torch.equal(ids[at:at + 2500], part) and torch.equal(w[at:at + 2500], pw)
     assert (ids >= 0).all() and ((w.sum(-1) - 2.5).abs() < 1e-5).all()
+
+
+@pytest.mark.parametrize("layout", [mx.ROWMAJOR, mx.TILED])
+@pytest.mark.parametrize("tokens,topk,experts,k,n", [(2, 64, 100, 128, 96), (5, 64, 100, 128, 96), (40, 17, 1024, 128, 64),
+                                                     (300, 12, 20, 128, 288), (90, 64, 64, 256, 40)])
+def test_products_of_many_choices_and_experts(tokens, topk, experts, k, n, layout):
+    products.test_up(tokens, topk, experts, k, n, True, layout)
+    products.test_down(tokens, topk, experts, k, n, layout)

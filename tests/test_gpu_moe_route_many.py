@@ -22,6 +22,18 @@ def test_route_where_lanes_change(tokens, experts, topk, groups):
     check_route(logits.to(BF), mx.Router(topk), "softmax")
 
 
+@pytest.mark.parametrize("tokens,experts,topk,groups,kept", [(20, 64, 10, 8, 1), (4100, 64, 10, 8, 1), (4100, 240, 16, 30, 1),
+                                                             (9, 1024, 64, 64, 3), (7, 130, 30, 13, 2)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_where_the_kept_groups_have_fewer_experts_than_choices(tokens, experts, topk, groups, kept, score):
+    gen = torch.Generator().manual_seed(tokens)
+    logits = torch.randn(tokens, experts, generator=gen).to(DEV)
+    for bias in (None, bias_of(experts)):
+        ids, w = check_route(logits, mx.Router(topk, score, bias, groups, kept, "max"), "few experts kept")
+        left = max(0, topk - experts // groups * kept)
+        assert ((ids == -1).sum(1) == left).all() and ((w == 0).sum(1) == left).all()
+
+
 @pytest.mark.parametrize("base", [-690.0, -703.0, -709.0, -720.0, -738.0])
 def test_weights_of_scores_near_binary64s_end(base):
     """Sigmoid scores down to 2^-1074: the chosen ones' ratio is that of e^l, each off
